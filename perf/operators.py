@@ -358,7 +358,7 @@ def _cache(s):
     if "handle" not in s:
         import query_union_paged_b200 as qup
         s["handle"] = qup.KVCache(s["K"], s["V"], s["k_scale"], s["v_scale"], s["page_table"], s["page_ptr"],
-                                  s["kv_len"])
+                                  s["kv_len"], max_pages=s["max_pages"])
         if s["case"]["op"] == "attn":
             s["out"] = torch.empty_like(s["q"])
             s["lse"] = torch.empty(s["q"].shape[:2], dtype=torch.float32, device=s["q"].device)
