@@ -51,6 +51,7 @@ extern "C" {
 #define QUP_ERR_PHYS_PAGE 16   /* device: a page_table entry outside [0, P_phys) */
 #define QUP_ERR_GROUP 32       /* device: a group with no members, too many rows or a bad query ID */
 #define QUP_ERR_TIMEOUT 64     /* device: a pipeline wait exceeded its limit; the kernel exited cleanly */
+#define QUP_ERR_SCALE 128      /* device: a cache scale that is not finite, or a negative V scale */
 
 /* dtype codes */
 #define QUP_F32 0
@@ -366,6 +367,122 @@ int qup_page_major_attn(const void* Q, int q_dtype, const void* K_cache, const v
                         int P_phys, int T, const qup_page_items* items, const int32_t* q_pos, int kv_len, int Hq,
                         int Hkv, int Nq, int d, float softmax_scale, float* part_o, float* part_lse, void* O,
                         float* lse, void* stream);
+
+/*
+ * An 8-bit KV cache with one scale per page and KV head, written, read and
+ * evicted by the three calls below (no counterpart on the pages, whose cache
+ * is given).  R sequences ("requests") share the physical pages:
+ *   K, V       device E4M3 [P_phys][Hkv][T][128], 16-byte aligned
+ *   k_scale, v_scale  device fp32 [P_phys][Hkv]: a byte x of page p and head
+ *              h stands for e4m3(x) * scale[p][h]
+ *   page_table device int32 [total_pages]; request r's logical pages are its
+ *              entries page_ptr[r] .. page_ptr[r+1) (those past its last token
+ *              are pages to grow into)
+ *   page_ptr   device int32 [R+1], ascending; kv_len device int32 [R]: tokens
+ *              of each request, at most its pages x T
+ *   max_pages  page table entries of one request, at most (1 .. total_pages);
+ *              attention and eviction refuse a request with more
+ * Two requests may share physical pages for reading; pages that
+ * qup_cache_append writes belong to one request.
+ */
+typedef struct {
+    void* K;
+    void* V;
+    float* k_scale;
+    float* v_scale;
+    const int32_t* page_table;
+    const int32_t* page_ptr;
+    const int32_t* kv_len;
+    int32_t P_phys, Hkv, T, R, total_pages, max_pages;
+} qup_cache;
+
+/*
+ * Writes new tokens into the cache.  The rows tok_ptr[r] .. tok_ptr[r+1) of
+ * k_new and v_new are request r's last tokens: positions kv_len[r] - n ..
+ * kv_len[r] - 1 with n = tok_ptr[r+1] - tok_ptr[r] (kv_len counts them
+ * already).  The scale of a page is a power of two: the smallest 2^k, k >= -64,
+ * with max|x| <= 448 * 2^k over the new tokens' finite values in the page and
+ * KV head; a page that holds older tokens keeps its scale if that is larger,
+ * else its older bytes are requantised to the new one.  A byte is x / scale
+ * rounded to nearest even; an infinity or NaN becomes NaN (0x7f) and does not
+ * count for the scale.  Slots past a request's last token are left as they are.
+ *   dtype     QUP_BF16 or QUP_F32 (k_new, v_new: [N][Hkv][128])
+ *   k_stride, v_stride  elements from one token to the next, a multiple of 8
+ *             (bf16) or 4 (fp32) and at least Hkv * 128; the pointers are
+ *             16-byte aligned (heads and elements are contiguous)
+ *   tok_ptr   device int32 [R+1], ascending; rows of no request are not read
+ * Device errors: QUP_ERR_GROUP for a request whose rows, length and pages
+ * contradict each other (nothing of it is written), QUP_ERR_PHYS_PAGE for a
+ * page_table entry out of range, QUP_ERR_SCALE for an old scale that is
+ * negative or not finite (that page is not written).
+ */
+int qup_cache_append(const qup_cache* cache, const void* k_new, const void* v_new, int dtype, int64_t k_stride,
+                     int64_t v_stride, const int32_t* tok_ptr, int N, int d, void* stream);
+
+/*
+ * Attention over the cache for single tokens (decode), short runs (drafted
+ * tokens, several at once) and chunks.  The rows q_ptr[r] .. q_ptr[r+1) of Q
+ * are request r's last positions, kv_len[r] - n .. kv_len[r] - 1; query i sees
+ * the tokens t <= its position, of all pages or of the pages in its TopK rows:
+ *   s_t = softmax_scale * (q . k_t) * k_scale,  O = sum softmax(s)_t v_t v_scale
+ * KV head of Q head h' is h' / (Hq / Hkv).
+ *   Q          device bf16 [Nq][Hq][128], q_stride elements from one query to
+ *              the next (a multiple of 8, at least Hq * 128), 16-byte aligned
+ *   max_q      queries of one request, at most
+ *   topk, Ksel device int32 [Hq][Nq][Ksel] logical pages of the query's own
+ *              request, -1 = padding (duplicates count once), or NULL for all
+ *              pages; Hq / Hkv <= 32 with topk
+ *   O          device bf16 [Nq][Hq][128], 16-byte aligned; rows of no request
+ *              are not written; a row that sees nothing gets 0
+ *   lse        device fp32 [Nq][Hq] natural-log sum of exponentials (-inf for a
+ *              row that sees nothing), or NULL
+ *   page_weight device fp32 [total_pages][Hkv] or NULL: the softmax weight that
+ *              the request's queries and the KV head's Q heads give each page
+ *              of the table, added up (0 for pages without visible tokens)
+ *   ws         device scratch of the size qup_cache_attn_workspace reports for
+ *              the same cache sizes, Nq, max_q, Hq and page_weight; calls that
+ *              may run at the same time need one each.  Its contents need no
+ *              preparation and mean nothing after the call.
+ * Results do not depend on the run: partial results are merged in a fixed
+ * order, without atomics.  Device errors: QUP_ERR_GROUP for a contradictory
+ * request or one with more than max_q queries (its rows get O = 0, lse = -inf),
+ * QUP_ERR_CAPACITY for a request with more than max_pages pages (likewise),
+ * QUP_ERR_PAGE_ID for a TopK entry outside the request's
+ * pages (ignored), QUP_ERR_PHYS_PAGE and QUP_ERR_SCALE for a bad page_table
+ * entry or scale (the page is not seen), QUP_ERR_TIMEOUT as elsewhere.
+ */
+int qup_cache_attn_workspace(const qup_cache* cache, int Nq, int max_q, int Hq, int page_weight, size_t* ws_bytes);
+int qup_cache_attn(const qup_cache* cache, const void* Q, int64_t q_stride, const int32_t* q_ptr, int Nq, int max_q,
+                   int Hq, int d, const int32_t* topk, int Ksel, float softmax_scale, void* O, float* lse,
+                   float* page_weight, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Eviction of whole pages by accumulated attention weight (per request; H2O-
+ * style heavy hitters at page granularity).  For every page that holds tokens
+ *   score[p] = decay * acc[p] + sum over heads of page_weight[p][h]
+ * (in 64 bits, rounded once).  If the request holds more than `budget` such
+ * pages, the lowest scores among those that are neither its first `sink` nor
+ * its last `recent` pages are dropped until `budget` remain or no page may go
+ * (equal scores: the lower page; NaN ranks highest); recent is at least 1, as
+ * the last page may be partly filled.  Kept pages move together
+ * in order, the dropped ones follow in order as pages to grow into, then the
+ * entries that held no tokens.  Physical pages do not move, so positions
+ * change: token t of a kept page moves with its page.
+ *   page_weight device fp32 [total_pages][Hkv]; acc device fp32 [total_pages]
+ *   table_out  device int32 [total_pages], the new page table; acc_out device
+ *              fp32 [total_pages], the scores in the new order (0 for dropped
+ *              pages, acc for unused entries); len_out device int32 [R], the
+ *              new kv_len; page_src device int32 [total_pages], the old
+ *              request-local place of each entry.  They may be cache's own
+ *              page_table and kv_len, and acc.  Entries of no request are left
+ *              as they are.
+ * Device errors: QUP_ERR_GROUP (contradictory request) and QUP_ERR_CAPACITY
+ * (more than max_pages pages): the request's entries are copied unchanged.
+ * QUP_ERR_ARG for max_pages beyond what one CTA's shared memory holds (24576).
+ */
+int qup_cache_evict(const qup_cache* cache, const float* page_weight, const float* acc, float decay, int budget,
+                    int sink, int recent, int32_t* table_out, float* acc_out, int32_t* len_out, int32_t* page_src,
+                    void* stream);
 
 /* Synchronizes `stream`, then reads and clears this device's error word. */
 int qup_get_error(int* code, void* stream);

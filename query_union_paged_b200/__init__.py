@@ -8,6 +8,14 @@ calls raise.
 
     groups = sparse_group(topk, Hq, Hkv, num_logical_pages, max_group=8, window=64)
     O = sparse_prefill_attn(Q, K_cache, V_cache, page_table, groups, q_pos, kv_len, ...)
+
+An 8-bit cache with a scale per page and KV head, for serving: written, read (single tokens, short
+runs, chunks) and evicted on the device.
+
+    cache = KVCache(K, V, k_scale, v_scale, page_table, page_ptr, kv_len)
+    cache_append(cache, k_new, v_new, tok_ptr)
+    O = cache_attn(cache, Q, q_ptr, max_q, topk=None, page_weight=w)
+    page_table, acc, kv_len, src = cache_evict(cache, w, acc, budget)
 """
 from __future__ import annotations
 
@@ -21,11 +29,12 @@ import numpy as np
 
 __all__ = ["Groups", "sparse_group", "sparse_prefill_attn", "build_bundles", "groups_from_host", "union_support",
            "Batch", "batch_prepare", "sparse_prefill_attn_batch", "PageItems", "page_major_items", "page_major_attn",
-           "get_error", "set_debug", "set_checked", "load",
+           "KVCache", "cache_append", "cache_attn", "cache_attn_workspace", "cache_evict", "get_error", "set_debug", "set_checked", "load",
            "QupError", "F32", "BF16", "E4M3", "ERR"]
 
 F32, BF16, E4M3 = 0, 1, 2
-ERR = {"ARG": 1, "CAPACITY": 2, "CUDA": 4, "PAGE_ID": 8, "PHYS_PAGE": 16, "GROUP": 32, "TIMEOUT": 64}
+ERR = {"ARG": 1, "CAPACITY": 2, "CUDA": 4, "PAGE_ID": 8, "PHYS_PAGE": 16, "GROUP": 32, "TIMEOUT": 64,
+       "SCALE": 128}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libqup.so")
@@ -47,6 +56,11 @@ class _Groups(ctypes.Structure):
     _fields_ = ([(k, ctypes.c_void_p) for k in _GROUP_KEYS] + [("cap_union", ctypes.c_int64)] +
                 [(k, ctypes.c_void_p) for k in _BUNDLE_KEYS] +
                 [("rows_per_group", ctypes.c_int32), ("bundle_window", ctypes.c_int32)])
+
+
+class _CacheStruct(ctypes.Structure):
+    _fields_ = ([(k, ctypes.c_void_p) for k in ("K", "V", "k_scale", "v_scale", "page_table", "page_ptr", "kv_len")] +
+                [(k, ctypes.c_int32) for k in ("P_phys", "Hkv", "T", "R", "total_pages", "max_pages")])
 
 
 def load():
@@ -83,7 +97,13 @@ def load():
     lib.qup_sparse_prefill_attn_batch.argtypes = [P, I, P, P, I, P, P, P, I, I, I, P, I,
                                                   ctypes.POINTER(_Groups), P, P, I, I, I, I,
                                                   ctypes.c_float, P, P, P]
-    for fn in ("qup_group_workspace", "qup_sparse_group", "qup_build_bundles", "qup_sparse_prefill_attn",
+    C = ctypes.POINTER(_CacheStruct)
+    lib.qup_cache_append.argtypes = [C, P, P, I, I64, I64, P, I, I, P]
+    lib.qup_cache_attn_workspace.argtypes = [C, I, I, I, I, ctypes.POINTER(SZ)]
+    lib.qup_cache_attn.argtypes = [C, P, I64, P, I, I, I, I, P, I, ctypes.c_float, P, P, P, P, SZ, P]
+    lib.qup_cache_evict.argtypes = [C, P, P, ctypes.c_float, I, I, I, P, P, P, P, P]
+    for fn in ("qup_cache_append", "qup_cache_attn_workspace", "qup_cache_attn", "qup_cache_evict",
+               "qup_group_workspace", "qup_sparse_group", "qup_build_bundles", "qup_sparse_prefill_attn",
                "qup_get_error", "qup_set_debug", "qup_num_sms", "qup_exp2_poly", "qup_union_support",
                "qup_set_checked", "qup_batch_prepare", "qup_sparse_prefill_attn_batch", "qup_page_major_workspace",
                "qup_page_major_items", "qup_page_major_attn", "qup_pivot_select"):
@@ -439,6 +459,181 @@ def sparse_prefill_attn_batch(Q, K_cache, V_cache, page_table, groups: Groups, b
                                              float(softmax_scale), _p(out), _p(lse), _stream_ptr(stream)),
            "qup_sparse_prefill_attn_batch")
     return out
+
+
+def _need(ok, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _whole(t, name: str, dtype, shape, device):
+    """t is a contiguous tensor of this type and shape on this device."""
+    _need(t.dtype == dtype, f"{name}: {dtype} wanted, got {t.dtype}")
+    _need(tuple(t.shape) == tuple(shape), f"{name}: shape {tuple(shape)} wanted, got {tuple(t.shape)}")
+    _need(t.is_contiguous(), f"{name} is not contiguous")
+    _need(t.device == device, f"{name} is on {t.device}, the cache on {device}")
+
+
+class KVCache:
+    """An 8-bit KV cache of R requests with one scale per (page, KV head): qup_cache in the C header.
+
+    K, V [P_phys][Hkv][T][128] uint8 or float8_e4m3fn; k_scale, v_scale fp32 [P_phys][Hkv];
+    page_table int32 [total_pages], request r's logical pages being the entries
+    page_ptr[r] .. page_ptr[r+1); page_ptr int32 [R+1]; kv_len int32 [R], the tokens of each request.
+    max_pages: page table entries of one request, at most (default: all of them).
+
+    The object keeps the tensors and passes their addresses: their contents may change (kv_len grows,
+    the page table is rewritten by cache_evict), the tensors may not be replaced.
+    """
+
+    __slots__ = ("K", "V", "k_scale", "v_scale", "page_table", "page_ptr", "kv_len", "max_pages", "device", "_c",
+                 "_ref")
+
+    def __init__(self, K, V, k_scale, v_scale, page_table, page_ptr, kv_len, max_pages: Optional[int] = None):
+        import torch
+        _need(K.dim() == 4 and K.shape[3] == 128, f"K: [P_phys][Hkv][T][128] wanted, got {tuple(K.shape)}")
+        P_phys, Hkv, T, _ = K.shape
+        dev = K.device
+        _need(K.dtype in (torch.uint8, torch.float8_e4m3fn), f"K: uint8 or float8_e4m3fn wanted, got {K.dtype}")
+        for t, name in ((K, "K"), (V, "V")):
+            _whole(t, name, K.dtype, K.shape, dev)
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            _whole(t, name, torch.float32, (P_phys, Hkv), dev)
+        for t, name in ((page_table, "page_table"), (page_ptr, "page_ptr"), (kv_len, "kv_len")):
+            _whole(t, name, torch.int32, (t.numel(),), dev)
+        _need(page_ptr.numel() == kv_len.numel() + 1, "page_ptr has one entry more than kv_len")
+        _need(T in (16, 32, 64, 128), f"page size {T}: 16, 32, 64 or 128 wanted")
+        _need(page_table.numel() > 0 and P_phys > 0, "an empty page table or cache")
+        if max_pages is None:
+            max_pages = page_table.numel()
+        _need(1 <= max_pages <= page_table.numel(), f"max_pages {max_pages}: 1 .. {page_table.numel()} wanted")
+        _need(dev.type == "cuda", f"the cache is on {dev}: CUDA tensors wanted")
+        self.K, self.V, self.k_scale, self.v_scale = K, V, k_scale, v_scale
+        self.page_table, self.page_ptr, self.kv_len = page_table, page_ptr, kv_len
+        self.max_pages, self.device = max_pages, dev
+        self._c = _CacheStruct(*[t.data_ptr() for t in (K, V, k_scale, v_scale, page_table, page_ptr, kv_len)],
+                               P_phys, Hkv, T, kv_len.numel(), page_table.numel(), max_pages)
+        self._ref = ctypes.byref(self._c)
+
+
+def _on(cache: KVCache, stream):
+    """The device the call runs on, and its stream (default: that device's current one)."""
+    import torch
+    s = stream if stream is not None else torch.cuda.current_stream(cache.device)
+    _need(s.device == cache.device, f"the stream is on {s.device}, the cache on {cache.device}")
+    return torch.cuda.device(cache.device), ctypes.c_void_p(s.cuda_stream)
+
+
+def cache_append(cache: KVCache, k_new, v_new, tok_ptr, stream=None):
+    """Write new tokens into the cache (qup_cache_append).
+
+    k_new, v_new [N][Hkv][128] bf16 or fp32 (a token's heads contiguous, any token stride that keeps 16-byte
+    rows); tok_ptr int32 [R+1]: rows tok_ptr[r] .. tok_ptr[r+1) are request r's last tokens, which
+    cache.kv_len counts already.  A page's scale grows when a new token needs it (its older tokens are
+    requantised).
+    """
+    import torch
+    c = cache._c
+    _need(k_new.dtype in (torch.bfloat16, torch.float32), f"k_new: bfloat16 or float32 wanted, got {k_new.dtype}")
+    for t, name in ((k_new, "k_new"), (v_new, "v_new")):
+        _need(t.dtype == k_new.dtype and t.dim() == 3 and t.shape == k_new.shape and t.shape[1:] == (c.Hkv, 128),
+              f"{name}: [N][{c.Hkv}][128] of {k_new.dtype} wanted, got {tuple(t.shape)} of {t.dtype}")
+        _need(t.shape[0] == 0 or (t.stride(2) == 1 and t.stride(1) == 128), f"{name}: a token's heads are not contiguous")
+        _need(t.device == cache.device, f"{name} is on {t.device}, the cache on {cache.device}")
+    _whole(tok_ptr, "tok_ptr", torch.int32, (c.R + 1,), cache.device)
+    N, least = k_new.shape[0], c.Hkv * 128
+    ks, vs = (k_new.stride(0), v_new.stride(0)) if N > 1 else (least, least)
+    guard, st = _on(cache, stream)
+    with guard:
+        _check(load().qup_cache_append(cache._ref, k_new.data_ptr(), v_new.data_ptr(),
+                                       BF16 if k_new.dtype == torch.bfloat16 else F32, ks, vs, tok_ptr.data_ptr(), N,
+                                       128, st), "qup_cache_append")
+
+
+def cache_attn_workspace(cache: KVCache, Nq: int, Hq: int, max_q: int, page_weight: bool = False):
+    """A workspace for cache_attn calls of these sizes on this cache (qup_cache_attn_workspace).  Calls that
+    may run at the same time, captured graphs among them, need one each."""
+    import torch
+    n = ctypes.c_size_t(0)
+    _check(load().qup_cache_attn_workspace(cache._ref, Nq, max_q, Hq, 1 if page_weight else 0, ctypes.byref(n)),
+           "qup_cache_attn_workspace")
+    return torch.empty(n.value, dtype=torch.uint8, device=cache.device)
+
+
+def cache_attn(cache: KVCache, Q, q_ptr, max_q: int, topk=None, softmax_scale: Optional[float] = None, out=None,
+               lse=None, page_weight=None, workspace=None, stream=None):
+    """Attention over the cache (qup_cache_attn): decode, short runs and chunks of queries.
+
+    Q [Nq][Hq][128] bf16 (a query's heads contiguous); q_ptr int32 [R+1]: rows q_ptr[r] .. q_ptr[r+1) are
+    request r's last positions, at most max_q of them; topk int32 [Hq][Nq][Ksel] logical pages of the query's
+    request (-1 = padding) or None for all pages.  Fills lse fp32 [Nq][Hq] and page_weight fp32
+    [total_pages][Hkv] if given.  Returns O [Nq][Hq][128] bf16.
+    """
+    import torch
+    c, dev = cache._c, cache.device
+    _need(Q.dtype == torch.bfloat16 and Q.dim() == 3 and Q.shape[2] == 128,
+          f"Q: [Nq][Hq][128] of bfloat16 wanted, got {tuple(Q.shape)} of {Q.dtype}")
+    Nq, Hq, _ = Q.shape
+    _need(Nq == 0 or (Q.stride(2) == 1 and Q.stride(1) == 128), "Q: a query's heads are not contiguous")
+    _need(Q.device == dev, f"Q is on {Q.device}, the cache on {dev}")
+    _whole(q_ptr, "q_ptr", torch.int32, (c.R + 1,), dev)
+    ksel = 0
+    if topk is not None:
+        ksel = topk.shape[-1]
+        _whole(topk, "topk", torch.int32, (Hq, Nq, ksel), dev)
+    if out is None:
+        out = torch.empty(Q.shape, dtype=Q.dtype, device=dev)
+    else:
+        _whole(out, "out", torch.bfloat16, Q.shape, dev)
+    if lse is not None:
+        _whole(lse, "lse", torch.float32, (Nq, Hq), dev)
+    if page_weight is not None:
+        _whole(page_weight, "page_weight", torch.float32, (c.total_pages, c.Hkv), dev)
+    if workspace is None:
+        workspace = cache_attn_workspace(cache, Nq, Hq, max_q, page_weight is not None)
+    else:
+        _whole(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(128)
+    guard, st = _on(cache, stream)
+    with guard:
+        _check(load().qup_cache_attn(cache._ref, Q.data_ptr(), Q.stride(0) if Nq > 1 else Hq * 128, q_ptr.data_ptr(),
+                                     Nq, max_q, Hq, 128, None if topk is None else topk.data_ptr(), ksel,
+                                     softmax_scale, out.data_ptr(), None if lse is None else lse.data_ptr(),
+                                     None if page_weight is None else page_weight.data_ptr(), workspace.data_ptr(),
+                                     workspace.numel(), st), "qup_cache_attn")
+    return out
+
+
+def cache_evict(cache: KVCache, page_weight, acc, budget: int, sink: int = 1, recent: int = 1, decay: float = 1.0,
+                out=None, stream=None):
+    """Evict whole pages by accumulated attention weight (qup_cache_evict).
+
+    page_weight fp32 [total_pages][Hkv] of the last cache_attn, acc fp32 [total_pages]: what each page has
+    gathered before.  A request with more than `budget` pages drops the lowest of decay * acc + sum of
+    page_weight, but none of its first `sink` and last `recent`.  Returns (page_table, acc, kv_len, page_src),
+    the compacted table, accumulator and lengths and each entry's old place in its request; `out` holds these
+    four tensors if given, which may be the cache's own page_table and kv_len, and acc.
+    """
+    import torch
+    c, dev = cache._c, cache.device
+    _whole(page_weight, "page_weight", torch.float32, (c.total_pages, c.Hkv), dev)
+    _whole(acc, "acc", torch.float32, (c.total_pages,), dev)
+    if out is None:
+        out = (torch.empty_like(cache.page_table), torch.empty_like(acc), torch.empty_like(cache.kv_len),
+               torch.empty_like(cache.page_table))
+    else:
+        for t, name, dtype, n in zip(out, ("page_table", "acc", "kv_len", "page_src"),
+                                     (torch.int32, torch.float32, torch.int32, torch.int32),
+                                     (c.total_pages, c.total_pages, c.R, c.total_pages)):
+            _whole(t, "out " + name, dtype, (n,), dev)
+    table, acc_out, lens, src = out
+    guard, st = _on(cache, stream)
+    with guard:
+        _check(load().qup_cache_evict(cache._ref, page_weight.data_ptr(), acc.data_ptr(), decay, budget, sink, recent,
+                                      table.data_ptr(), acc_out.data_ptr(), lens.data_ptr(), src.data_ptr(), st),
+               "qup_cache_evict")
+    return table, acc_out, lens, src
 
 
 def exp2_poly(x, out=None, stream=None):

@@ -19,7 +19,7 @@ NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17", "--use_fast_math",
     "-Xcompiler", "-fPIC", "-shared",
-    "-Xptxas", "-warn-spills",
+    "-Xptxas", "-warn-spills", "--threads", "0",
 ]
 
 

@@ -10,6 +10,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "cache.h"
 #include "internal.h"
 #include "select.h"
 #include "query_union_paged.h"
@@ -47,10 +48,7 @@ std::atomic<int> g_skip_stage{-1};
 std::atomic<int> g_checked{0};  // checked mode: attention validates the row masks against topk
 std::atomic<unsigned> g_walk_slot{0};  // the next launch slot of the attention kernel's bundle counter
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiledFn g_encode = nullptr;
+qup::TensorMapEncodeFn g_encode = nullptr;
 
 int device_state(DevState** out) {
     int dev = 0;
@@ -73,7 +71,7 @@ int device_state(DevState** out) {
             if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q) != cudaSuccess ||
                 q != cudaDriverEntryPointSuccess || fn == nullptr)
                 return QUP_ERR_CUDA;
-            g_encode = reinterpret_cast<EncodeTiledFn>(fn);
+            g_encode = reinterpret_cast<qup::TensorMapEncodeFn>(fn);
         }
         s.ctx = ctx;
     }
@@ -508,8 +506,7 @@ int attn_impl(const void* Q, int q_dtype, const void* K_cache, const void* V_cac
     p.bstride = wk.bstride;
     p.nsk = nsk;
     p.nsv = nsv;
-    const int wait_ms = g_wait_limit_ms.load();
-    p.wait_limit_ns = (unsigned long long)(wait_ms > 0 ? wait_ms : 2000) * 1000000ull;
+    p.wait_limit_ns = qup::wait_limit_ns();
     p.dbg_skip_stage = g_skip_stage.load();
     p.walk_slot = (int)(g_walk_slot.fetch_add(1u) % (unsigned)qup::kWalkSlots);
     const cudaError_t e =
@@ -716,6 +713,7 @@ const char* qup_error_string(int code) {
         case QUP_ERR_PHYS_PAGE: return "page_table entry out of range";
         case QUP_ERR_GROUP: return "malformed group";
         case QUP_ERR_TIMEOUT: return "pipeline wait timed out";
+        case QUP_ERR_SCALE: return "cache scale is not a finite number in range";
         default: return "multiple errors (bitwise OR of codes)";
     }
 }
@@ -745,6 +743,19 @@ int qup_exp2_poly(const float* x, float* y, int n, void* stream) {
 }  // extern "C"
 
 namespace qup {
+
+int device_info(DeviceInfo* out) {
+    DevState* ds = nullptr;
+    const int rc = device_state(&ds);
+    if (rc) return rc;
+    *out = DeviceInfo{ds->err, ds->sms, ds->smem_optin, g_encode};
+    return QUP_OK;
+}
+
+unsigned long long wait_limit_ns() {
+    const int ms = g_wait_limit_ms.load();
+    return (unsigned long long)(ms > 0 ? ms : 2000) * 1000000ull;
+}
 
 unsigned long long context_id() {
     typedef CUresult (*GetCurrentFn)(CUcontext*);

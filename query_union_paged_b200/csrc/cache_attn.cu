@@ -1,0 +1,989 @@
+// cache_attn.cu -- attention over the 8-bit page-scaled cache: single tokens and short runs of
+// queries, over all pages of a request or over each query's TopK pages.
+//
+// Per row (query i, query head j of KV head h) and visible token t of page p:
+//   s_t = softmax_scale * (q . k_t) * ks[p][h],  O = sum e^{s_t} vs[p][h] v_t / sum e^{s_t},
+// with k_t, v_t the E4M3 values.  One pass with a running maximum over x_t = log2e s_t + log2 vs:
+//   p'_t = 2^{x_t - m + 8},  O += p'_t v_t,  l += p'_t / vs,
+// so the V scale costs nothing per element and P has one range whatever the scales are.
+//
+// Numbers: E4M3 is exact in fp16; Q (bf16) is brought to fp16 by a power of two per row (its largest
+// element in [2^14, 2^15): what rounds lies 2^-31 below it), P is rounded to fp16 (2^-11; the
+// offset 8 keeps weights down to 2^-32 of the largest).  Products accumulate in fp32.
+//
+// Layout: a work unit is 64 tokens of one KV head: 8 KB of K and 8 KB of V, streamed by one
+// producer warp with TMA (128-byte swizzle) through a ring of stages.  Each of the four consumer
+// warps takes 16 tokens of every unit with its own running maximum, sum and output (no exchange
+// inside the loop), 16 or 32 rows per tile as mma.m16n8k16 operands straight from the bytes: the
+// order of d inside K's fragments and of d over the output columns is free, so every lane reads 16
+// consecutive bytes of a token (conflict-free under the swizzle) and converts two values at a time.
+// The warps merge in shared memory at the end of a segment.
+//
+// Work split: all pages: the units of all (request, KV head, row tile) items are laid end to end and
+// cut into equal runs, one per CTA, so ragged lengths balance; an item cut across CTAs leaves one
+// partial result in each, which a second kernel merges in a fixed order.  TopK pages: one item per
+// (query, KV head), its distinct pages cut into an equal share per CTA.
+//
+// Bound by DRAM: 2 * 128 bytes per token and KV head.
+#include <algorithm>
+#include <cstdint>
+
+#include "cache.h"
+#include "cache_attn.h"
+#include "internal.h"
+#include "ptx.cuh"
+#include "query_union_paged.h"
+
+namespace qup {
+namespace {
+
+constexpr int kUnit = kCacheUnit;               // tokens of a work unit
+constexpr int kTile = kUnit * kHeadDim;         // bytes of one K or V tile
+constexpr int kConsumers = 4;                   // consumer warps: kUnit / 16 tokens
+constexpr int kThreads = 32 * (kConsumers + 1);
+constexpr int kMaxBoxes = kUnit / 16;           // pages in a unit at T = 16
+constexpr float kOffset = 8.f;                  // log2 offset of P
+constexpr float kLazy = 7.f;                    // the maximum moves once a score passes it by this
+constexpr float kZeroScaleLog2 = -64.f;         // a V scale of 0 (a page of zeros) counts as 2^-64
+constexpr float kNegInf = -INFINITY;
+
+// A page of a stage, as the consumers need it.
+struct PageMeta {
+    float ks;        // softmax_scale * log2e is in the row's factor
+    float vs_log2;
+    float vs_inv;
+    uint32_t mask;   // bit per row of the tile's first 32 (TopK: the query heads); all ones otherwise
+    int pos;         // position of the page's first token in the unit
+    int pad[3];
+};
+
+__device__ __forceinline__ uint32_t cvt_e4m3x2(uint32_t v) {  // low 16 bits
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)v));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ bool has_nan_byte(uint32_t w) {  // an E4M3 NaN (0x7f or 0xff) among four
+    const uint32_t x = (w & 0x7f7f7f7fu) + 0x01010101u;
+    return (x & 0x80808080u) != 0u;
+}
+
+// Work units of one row tile of a request, and its row tiles.
+__device__ __forceinline__ int units_of(int len) { return (len + kUnit - 1) / kUnit; }
+__device__ __forceinline__ int tiles_of(int n, int g, int RT) { return (n * g + RT - 1) / RT; }
+
+// The requests' unit counts added up: this thread's sum over its own consecutive requests, then the
+// CTA's exclusive prefix (in `part`, kThreads entries).  total in *all.
+struct Span {
+    int r0, r1;
+};
+__device__ __forceinline__ Span my_span(int R) {
+    const int per = (R + kThreads - 1) / kThreads;
+    const int a = min(R, (int)threadIdx.x * per);
+    return Span{a, min(R, a + per)};
+}
+__device__ __forceinline__ unsigned request_fault(const CacheAttnParams& p, const Request& q) {
+    if (!q.ok || q.n > p.max_q) return QUP_ERR_GROUP;
+    return q.np > p.max_pages ? QUP_ERR_CAPACITY : 0u;
+}
+__device__ __forceinline__ int request_units(const CacheAttnParams& p, int r, int RT, unsigned* bad) {
+    const Request q = load_request(p.q_ptr, p.Nq, p.c.kv_len, p.c.page_ptr, p.c.total_pages, p.c.T, r);
+    const unsigned f = request_fault(p, q);
+    *bad |= f;
+    return f ? 0 : tiles_of(q.n, p.g, RT) * p.c.Hkv * units_of(q.len);
+}
+
+// Units of one CTA's run: an equal share of all of them.
+__device__ __forceinline__ int units_per_cta(const CacheAttnParams& p, long long all, int grid) {
+    return max(p.per_units, (int)((all + grid - 1) / grid));
+}
+
+// Where a CTA's run of units begins, and how long it is.
+struct Start {
+    int r, off, count;
+};
+
+// One item's view of the cache while it is walked: a segment [b0, b1) of its units.
+struct Seg {
+    int r, q0, n, len, p0, np;
+    int h, tile, b0, b1, nvis;  // nvis: units that the tile's last row sees any token of
+};
+
+// Walks the units [off, ...) of requests r, r + 1, ... in (KV head, row tile, unit) order.
+struct Cursor {
+    int r, off, left;
+    Request q;
+    int nb, nt;
+    __device__ __forceinline__ void begin(const Start& s) {
+        r = s.r;
+        off = s.off;
+        left = s.count;
+        nb = -1;
+    }
+    __device__ __forceinline__ bool next(const CacheAttnParams& p, int RT, Seg& s) {
+        while (left > 0) {
+            if (nb < 0) {
+                if (r >= p.c.R) return false;
+                q = load_request(p.q_ptr, p.Nq, p.c.kv_len, p.c.page_ptr, p.c.total_pages, p.c.T, r);
+                const bool ok = request_fault(p, q) == 0u;
+                nb = ok ? units_of(q.len) : 0;
+                nt = ok ? tiles_of(q.n, p.g, RT) : 0;
+            }
+            const int total = nt * p.c.Hkv * nb;
+            if (off >= total) {
+                off -= total;
+                ++r;
+                nb = -1;
+                continue;
+            }
+            const int it = off / nb;
+            s.r = r;
+            s.q0 = q.q0;
+            s.n = q.n;
+            s.len = q.len;
+            s.p0 = q.p0;
+            s.np = q.np;
+            s.h = it / nt;
+            s.tile = it - s.h * nt;
+            s.b0 = off - it * nb;
+            s.b1 = min(nb, s.b0 + left);
+            off += s.b1 - s.b0;
+            left -= s.b1 - s.b0;
+            const int last = (min((s.tile + 1) * RT, s.n * p.g) - 1) / p.g;  // the tile's last query
+            const int vis = s.len - s.n + last + 1;
+            s.nvis = vis <= 0 ? 0 : units_of(vis);
+            return true;
+        }
+        return false;
+    }
+};
+
+// Shared memory, from a 1024-byte boundary: the ring, then what follows.
+template <int MT>
+struct Smem {
+    static constexpr int RT = 16 * MT;
+    static constexpr int kStages = MT == 1 ? 6 : 5;
+    static constexpr uint32_t ring = 0;
+    static constexpr uint32_t out = ring + kStages * 2 * kTile;             // [RT][128] fp32
+    static constexpr uint32_t qfrag = out + RT * kHeadDim * 4;              // MT > 1: [MT][8][32] uint4
+    static constexpr uint32_t meta = qfrag + (MT > 1 ? RT * kHeadDim * 2 : 0);  // [kStages][kMaxBoxes]
+    static constexpr uint32_t ml = meta + kStages * kMaxBoxes * sizeof(PageMeta);  // [kConsumers][RT] float2
+    static constexpr uint32_t bars = ml + kConsumers * RT * 8;
+    static constexpr uint32_t misc = bars + 2 * kStages * 8;  // abort flag, start, scan
+    static constexpr uint32_t list = misc + 64 + 8 * kThreads;  // TopK: bitmap, prefix, pages, masks
+};
+
+template <int MT, bool SPARSE, bool WEIGHTS>
+__global__ void __launch_bounds__(kThreads, 2)
+    cache_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                      const __grid_constant__ CacheAttnParams p) {
+    using L = Smem<MT>;
+    constexpr int RT = L::RT, NS = L::kStages;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t full0 = sbase + L::bars, empty0 = full0 + 8 * NS;
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::misc);
+    int* s_start = reinterpret_cast<int*>(smem + L::misc + 16);  // r, off, count
+    long long* scan = reinterpret_cast<long long*>(smem + L::misc + 64);
+    PageMeta* meta = reinterpret_cast<PageMeta*>(smem + L::meta);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int T = p.c.T, g = p.g;
+    const int box = min(T, kUnit), nbox = kUnit / box;
+    if (tid == 0) {
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(full0 + 8 * s, 1);
+            mbar_init(empty0 + 8 * s, kConsumers);
+        }
+        *abort_flag = 0;
+        s_start[0] = p.c.R;
+        s_start[1] = 0;
+        s_start[2] = 0;
+        fence_mbar_init();
+    }
+    if (warp == kConsumers && lane == 0) {
+        prefetch_tensormap(&tmK);
+        prefetch_tensormap(&tmV);
+    }
+    grid_dep_wait();
+    __syncthreads();
+
+    // ---------------------------------------------------------------- this CTA's work
+    Seg sg;                  // TopK: the one segment
+    int list_lo = 0, list_n = 0;
+    uint32_t *bits = nullptr, *masks = nullptr;
+    int *before = nullptr, *pages = nullptr;
+    if constexpr (!SPARSE) {
+        const Span sp = my_span(p.c.R);
+        long long sum = 0;
+        unsigned bad = 0;
+        for (int r = sp.r0; r < sp.r1; ++r) sum += request_units(p, r, RT, &bad);
+        if (bad) atomicOr(p.err, bad);
+        scan[tid] = sum;
+        __syncthreads();
+        long long mine = 0, all = 0;
+        for (int t = 0; t < kThreads; ++t) {
+            mine += t < tid ? scan[t] : 0;
+            all += scan[t];
+        }
+        const int per = units_per_cta(p, all, (int)gridDim.x);
+        const long long u0 = (long long)blockIdx.x * per;
+        if (u0 < all) {
+            if (u0 >= mine && u0 < mine + sum) {
+                long long at = mine;
+                for (int r = sp.r0; r < sp.r1; ++r) {
+                    const int u = request_units(p, r, RT, &bad);
+                    if (u0 < at + u) {
+                        s_start[0] = r;
+                        s_start[1] = (int)(u0 - at);
+                        s_start[2] = (int)min((long long)per, all - u0);
+                        break;
+                    }
+                    at += u;
+                }
+            }
+        }
+        __syncthreads();
+        if (s_start[2] == 0) return;
+    } else {
+        // the item's query and request
+        const int item = blockIdx.x / p.nsplit, split = blockIdx.x - item * p.nsplit;
+        const int qi = item / p.c.Hkv, h = item - qi * p.c.Hkv;
+        for (int r = tid; r < p.c.R; r += kThreads)
+            if (p.q_ptr[r] <= qi && qi < p.q_ptr[r + 1]) s_start[0] = r;
+        __syncthreads();
+        const int r = s_start[0];
+        if (r >= p.c.R) return;  // a row of no request: left as it is
+        const Request q = load_request(p.q_ptr, p.Nq, p.c.kv_len, p.c.page_ptr, p.c.total_pages, T, r);
+        const unsigned fault = request_fault(p, q);
+        const bool ok = fault == 0u;
+        if (!ok && tid == 0) atomicOr(p.err, fault);
+        const int vis = ok ? q.len - q.n + (qi - q.q0) + 1 : 0;  // tokens the query sees
+        const int words = ok ? (q.np + 31) / 32 : 0;
+        bits = reinterpret_cast<uint32_t*>(smem + L::list);
+        before = reinterpret_cast<int*>(bits + (p.max_pages + 31) / 32);
+        pages = before + (p.max_pages + 31) / 32;
+        masks = reinterpret_cast<uint32_t*>(pages + p.list_cap);
+        for (int w = tid; w < words; w += kThreads) bits[w] = 0u;
+        __syncthreads();
+        const int entries = g * p.Ksel;
+        for (int e = tid; e < entries; e += kThreads) {
+            const int j = e / p.Ksel, k = e - j * p.Ksel;
+            const int pg = __ldg(p.topk + ((size_t)(h * g + j) * p.Nq + qi) * p.Ksel + k);
+            if (pg == -1) continue;
+            if (pg < 0 || (ok && pg >= q.np)) {
+                atomicOr(p.err, QUP_ERR_PAGE_ID);
+                continue;
+            }
+            if ((long long)pg * T < vis) atomicOr(&bits[pg >> 5], 1u << (pg & 31));
+        }
+        __syncthreads();
+        {  // pages before each bitmap word
+            const int per = (words + kThreads - 1) / kThreads, w0 = min(words, tid * per), w1 = min(words, w0 + per);
+            int sum = 0;
+            for (int w = w0; w < w1; ++w) {
+                before[w] = sum;
+                sum += __popc(bits[w]);
+            }
+            scan[tid] = sum;
+            __syncthreads();
+            int mine = 0, all = 0;
+            for (int t = 0; t < kThreads; ++t) {
+                mine += t < tid ? (int)scan[t] : 0;
+                all += (int)scan[t];
+            }
+            for (int w = w0; w < w1; ++w) before[w] += mine;
+            const int share = (all + p.nsplit - 1) / p.nsplit;
+            list_lo = min(all, split * share);
+            list_n = min(all, list_lo + share) - list_lo;
+            for (int x = tid; x < list_n; x += kThreads) masks[x] = 0u;
+            if (WEIGHTS && split == 0 && ok) {  // which pages this query reads, for the page weights
+                uint32_t* dst = p.ws_bits + ((size_t)(q.p0 / 32 + r) * p.max_q * p.c.Hkv) +
+                                ((size_t)(qi - q.q0) * p.c.Hkv + h) * ((q.np + 31) / 32);
+                for (int w = tid; w < (q.np + 31) / 32; w += kThreads) dst[w] = bits[w];
+            }
+        }
+        __syncthreads();
+        for (int e = tid; e < entries; e += kThreads) {
+            const int j = e / p.Ksel, k = e - j * p.Ksel;
+            const int pg = __ldg(p.topk + ((size_t)(h * g + j) * p.Nq + qi) * p.Ksel + k);
+            if (pg < 0 || pg >= q.np || (long long)pg * T >= vis) continue;
+            const int at = before[pg >> 5] + __popc(bits[pg >> 5] & ((1u << (pg & 31)) - 1u)) - list_lo;
+            if (at < 0 || at >= list_n) continue;
+            pages[at] = pg;
+            atomicOr(&masks[at], 1u << j);
+        }
+        __syncthreads();
+        sg.r = r;
+        sg.q0 = qi;
+        sg.n = 1;
+        sg.len = vis;  // the query is the last of its visible tokens
+        sg.p0 = q.p0;
+        sg.np = q.np;
+        sg.h = h;
+        sg.tile = split;
+        sg.b0 = 0;
+        sg.b1 = sg.nvis = T > kUnit ? list_n * (T / kUnit) : (list_n + nbox - 1) / nbox;
+    }
+
+    Cursor cur;
+    if constexpr (!SPARSE) cur.begin(Start{s_start[0], s_start[1], s_start[2]});
+    bool more = SPARSE;
+    uint32_t it = 0;  // stages used so far: slot it % NS, parity (it / NS) & 1
+    bool dead = false;
+
+    if (warp == kConsumers) {
+        // ============================================================ producer
+        while (SPARSE ? more : cur.next(p, RT, sg)) {
+            more = false;
+            const int e0 = sg.b0, e1 = min(sg.b1, sg.nvis);  // units that are read
+            // 32 pages at a time: each lane looks one up
+            const int upp = T > kUnit ? T / kUnit : 1;  // units per page, or pages per unit
+            const int ppu = T > kUnit ? 1 : nbox;
+            int have0 = 0, have1 = 0;  // page entries the lanes hold
+            int phys = -1, lpos = 0;
+            float ks = 0.f, vl = 0.f, vi = 0.f;
+            uint32_t msk = 0;
+            for (int b = e0; b < e1 && !dead; ++b) {
+                const int pe = b / upp * ppu;  // the unit's first page entry
+                if (pe + ppu > have1) {
+                    have0 = pe;
+                    have1 = pe + 32;
+                    const int e = pe + lane;
+                    const int last = SPARSE ? list_n : (sg.len + T - 1) / T;
+                    phys = -1;
+                    msk = 0;
+                    lpos = 0x40000000;  // no page: past every row's visible tokens
+                    if (e < last) {
+                        const int pg = SPARSE ? pages[e] : e;
+                        msk = SPARSE ? masks[e] : 0xffffffffu;
+                        lpos = pg * T;
+                        phys = p.c.page_table[sg.p0 + pg];
+                        if (phys < 0 || phys >= p.c.P_phys) {
+                            atomicOr(p.err, QUP_ERR_PHYS_PAGE);
+                            phys = -1;
+                        } else {
+                            ks = __ldg(p.c.k_scale + (size_t)phys * p.c.Hkv + sg.h);
+                            const float vs = __ldg(p.c.v_scale + (size_t)phys * p.c.Hkv + sg.h);
+                            if (!(fabsf(ks) < INFINITY) || !(vs >= 0.f && vs < INFINITY)) {
+                                atomicOr(p.err, QUP_ERR_SCALE);
+                                phys = -1;
+                            }
+                            vl = vs > 0.f ? lg2(vs) : kZeroScaleLog2;
+                            vi = vs > 0.f ? __frcp_rn(vs) : 18446744073709551616.f;
+                        }
+                    }
+                    if (phys < 0) msk = 0;
+                }
+                const uint32_t slot = it % NS, par = (it / NS) & 1;
+                if (!mbar_wait(empty0 + 8 * slot, par ^ 1, abort_flag, p.err, QUP_ERR_TIMEOUT, p.wait_limit_ns)) {
+                    dead = true;
+                    break;
+                }
+                const int src = pe - have0;
+                uint32_t bytes = 0;
+                for (int x = 0; x < nbox; ++x) {
+                    const int ph = __shfl_sync(0xffffffffu, phys, src + x);
+                    bytes += ph >= 0 ? 2u * box * kHeadDim : 0u;
+                    if (lane == src + x) {
+                        PageMeta m;
+                        m.ks = ks;
+                        m.vs_log2 = vl;
+                        m.vs_inv = vi;
+                        m.mask = msk;
+                        m.pos = lpos + (b % upp) * kUnit;
+                        meta[slot * kMaxBoxes + x] = m;
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    if (bytes) mbar_arrive_expect_tx(full0 + 8 * slot, bytes);
+                    else mbar_arrive(full0 + 8 * slot);
+                }
+                __syncwarp();
+                for (int x = 0; x < nbox; ++x) {
+                    const int ph = __shfl_sync(0xffffffffu, phys, src + x);
+                    if (ph >= 0 && lane == 0) {
+                        const uint32_t dst = sbase + L::ring + slot * 2 * kTile + x * box * kHeadDim;
+                        tma_load_4d(dst, &tmK, full0 + 8 * slot, 0, (b % upp) * kUnit, sg.h, ph);
+                        tma_load_4d(dst + kTile, &tmV, full0 + 8 * slot, 0, (b % upp) * kUnit, sg.h, ph);
+                    }
+                }
+                ++it;
+            }
+        }
+        // a run that was given up: what is in flight lands before the CTA leaves
+        if (*abort_flag) {
+            for (uint32_t k = it > NS ? it - NS : 0; k < it; ++k)
+                mbar_wait_drain(full0 + 8 * (k % NS), (k / NS) & 1, p.wait_limit_ns);
+        }
+        return;
+    }
+
+    // ================================================================ consumers
+    const int i = lane >> 2, q4 = lane & 3;
+    float* s_out = reinterpret_cast<float*>(smem + L::out);
+    float2* s_ml = reinterpret_cast<float2*>(smem + L::ml);
+    uint4* s_q = reinterpret_cast<uint4*>(smem + L::qfrag);
+    bool first_seg = true;
+    while (SPARSE ? more : cur.next(p, RT, sg)) {
+        more = false;
+        const int rows = SPARSE ? g : min(RT, sg.n * g - sg.tile * RT);  // rows of the tile
+        const int row0 = SPARSE ? 0 : sg.tile * RT;                     // in (query, head) order
+        const int e0 = sg.b0, e1 = min(sg.b1, sg.nvis);
+        // ---- Q fragments: lane (i, q4) holds d = 32 q4 + 4 ks .. + 3 of rows i and i + 8
+        uint32_t qa[MT == 1 ? 8 : 1][4];
+        float rs[MT][2];
+        int vis[MT][2];  // tokens each row sees
+        float m[MT][2], l[MT][2], o[MT][16][4];
+        if (MT > 1) bar_sync(1, 32 * kConsumers);  // the last segment's fragments are done with
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            uint32_t f[8][4];
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const int rr = 16 * mt + 8 * hf + i;
+                const bool on = rr < rows;
+                const int x = row0 + (on ? rr : 0), qi = SPARSE ? 0 : x / g, j = x - qi * g;
+                const uint4* src = reinterpret_cast<const uint4*>(
+                    static_cast<const uint16_t*>(p.Q) + (size_t)(sg.q0 + qi) * p.q_stride +
+                    (size_t)(sg.h * g + j) * kHeadDim + 32 * q4);
+                uint4 raw[4];
+                uint32_t top = 0;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    raw[u] = on ? __ldg(src + u) : make_uint4(0u, 0u, 0u, 0u);
+                    const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) top = max(top, max((w[e] << 16) & 0x7f800000u, w[e] & 0x7f800000u));
+                }
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                // the row's largest element is in [2^e, 2^(e+1)): times 2^(14 - e)
+                const int ex = max((int)(top >> 23) - 127, -100);
+                const float up = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
+                rs[mt][hf] = p.scale_log2 * __uint_as_float((uint32_t)(ex - 14 + 127) << 23);
+                vis[mt][hf] = on ? (SPARSE ? sg.len : sg.len - sg.n + qi + 1) : 0;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)  // word 4u + e: k-step 2u + e / 2, register half e & 1
+                        f[2 * u + e / 2][hf + 2 * (e & 1)] = pack_f16x2(__uint_as_float(w[e] << 16) * up,
+                                                                       __uint_as_float(w[e] & 0xffff0000u) * up);
+                }
+                m[mt][hf] = kNegInf;
+                l[mt][hf] = 0.f;
+            }
+            if constexpr (MT == 1) {
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) qa[s][e] = f[s][e];
+            } else if (warp == mt) {
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                    s_q[(mt * 8 + s) * 32 + lane] = make_uint4(f[s][0], f[s][1], f[s][2], f[s][3]);
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[mt][j][e] = 0.f;
+        }
+        if (MT > 1) bar_sync(1, 32 * kConsumers);
+        // tokens that every row of the tile sees, and that any row sees
+        const int vis_all = SPARSE ? sg.len : sg.len - sg.n + row0 / g + 1;
+        const int vis_any = SPARSE ? sg.len : sg.len - sg.n + (row0 + rows - 1) / g + 1;
+        const uint32_t all_rows = SPARSE ? (rows == 32 ? 0xffffffffu : (1u << rows) - 1u) : 0xffffffffu;
+
+        for (int b = e0; b < e1; ++b, ++it) {
+            const uint32_t slot = it % NS, par = (it / NS) & 1;
+            if (!dead && !mbar_wait(full0 + 8 * slot, par, abort_flag, p.err, QUP_ERR_TIMEOUT, p.wait_limit_ns))
+                dead = true;
+            if (dead) continue;
+            const PageMeta pm = meta[slot * kMaxBoxes + 16 * warp / box];
+            const int pos = pm.pos + (16 * warp) % box;  // of the warp's first token
+            if (pm.mask != 0u && pos < vis_any) {
+                const uint32_t kt = sbase + L::ring + slot * 2 * kTile, vt = kt + kTile;
+                // ---- S = Q K^T: token 8 nt + i of the warp, d = 32 q4 .. + 31 of it in two loads
+                float c[MT][2][4];
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) {
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) c[mt][nt][e] = 0.f;
+                    const uint32_t row = kt + (16 * warp + 8 * nt + i) * kHeadDim;
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        const uint4 k = lds128(row + (((2 * q4 + s) ^ i) << 4));
+                        const uint32_t w[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t b0 = cvt_e4m3x2(w[e]), b1 = cvt_e4m3x2(w[e] >> 16);
+                            if constexpr (MT == 1) {
+                                mma16816(c[0][nt], qa[4 * s + e], b0, b1);
+                            } else {
+#pragma unroll
+                                for (int mt = 0; mt < MT; ++mt) {
+                                    const uint4 a = s_q[(mt * 8 + 4 * s + e) * 32 + lane];
+                                    const uint32_t aw[4] = {a.x, a.y, a.z, a.w};
+                                    mma16816(c[mt][nt], aw, b0, b1);
+                                }
+                            }
+                        }
+                    }
+                }
+                const bool mixed = pos + 16 > vis_all || (pm.mask & all_rows) != all_rows;
+                uint32_t pa[MT][4];
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const float f = rs[mt][hf] * pm.ks;
+                        float x[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[e] = fmaf(c[mt][e >> 1][2 * hf + (e & 1)], f, pm.vs_log2);
+                        if (mixed) {
+                            const int rr = 16 * mt + 8 * hf + i;
+                            const bool on = !SPARSE || ((pm.mask >> (rr & 31)) & 1u);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (!on || pos + 8 * (e >> 1) + 2 * q4 + (e & 1) >= vis[mt][hf]) x[e] = kNegInf;
+                        }
+                        float bm = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+                        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 1));
+                        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 2));
+                        if (__any_sync(0xffffffffu, bm > m[mt][hf] + kLazy)) {
+                            const bool mv = bm > m[mt][hf] + kLazy;  // -inf + kLazy = -inf
+                            const float a = mv ? ex2(m[mt][hf] - bm) : 1.f;
+                            if (mv) m[mt][hf] = bm;
+                            l[mt][hf] *= a;
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                o[mt][j][2 * hf] *= a;
+                                o[mt][j][2 * hf + 1] *= a;
+                            }
+                        }
+                        const float sub = m[mt][hf] == kNegInf ? 0.f : m[mt][hf] - kOffset;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[e] = ex2(x[e] - sub);
+                        float sum = ((x[0] + x[1]) + (x[2] + x[3])) * pm.vs_inv;
+                        l[mt][hf] += sum;
+                        if constexpr (WEIGHTS) {
+                            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                            const int rr = 16 * mt + 8 * hf + i;
+                            if (q4 == 0 && rr < rows) {
+                                const size_t rowsw = (size_t)p.max_q * g;
+                                const size_t at = ((size_t)sg.p0 * p.c.Hkv + (size_t)sg.h * sg.np) * (T / 16) * rowsw +
+                                                  (size_t)(pos / 16) * rowsw +
+                                                  (SPARSE ? (sg.q0 - p.q_ptr[sg.r]) * g : row0) + rr;
+                                p.ws_mass[at] = make_float2(sum, m[mt][hf]);
+                            }
+                        }
+                        pa[mt][hf] = pack_f16x2(x[0], x[1]);
+                        pa[mt][hf + 2] = pack_f16x2(x[2], x[3]);
+                    }
+                }
+                // ---- O += P V: tokens 2 q4, + 1, + 8, + 9 of the warp, d = 16 i .. + 15 of each
+                uint32_t v[4][4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int t = 2 * q4 + (e & 1) + 8 * (e >> 1);
+                    const uint4 w = lds128(vt + (16 * warp + t) * kHeadDim + ((i ^ (t & 7)) << 4));
+                    v[e][0] = w.x;
+                    v[e][1] = w.y;
+                    v[e][2] = w.z;
+                    v[e][3] = w.w;
+                }
+                bool slow = false;
+                if (mixed) {
+                    // bytes behind the last visible token may be anything; a NaN that some rows see and
+                    // others do not must not reach the others as 0 * NaN
+                    bool nan = false;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (pos + 2 * q4 + (e & 1) + 8 * (e >> 1) >= vis_any) v[e][0] = v[e][1] = v[e][2] = v[e][3] = 0u;
+                        nan = nan || has_nan_byte(v[e][0]) || has_nan_byte(v[e][1]) || has_nan_byte(v[e][2]) ||
+                              has_nan_byte(v[e][3]);
+                    }
+                    slow = __any_sync(0xffffffffu, nan);
+                }
+                if (!slow) {
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+#pragma unroll
+                        for (int hi = 0; hi < 2; ++hi) {
+                            const uint32_t x0 = __byte_perm(v[0][w], v[1][w], hi ? 0x7362 : 0x5140);
+                            const uint32_t x1 = __byte_perm(v[2][w], v[3][w], hi ? 0x7362 : 0x5140);
+#pragma unroll
+                            for (int d = 0; d < 2; ++d) {
+                                const uint32_t b0 = cvt_e4m3x2(d ? x0 >> 16 : x0), b1 = cvt_e4m3x2(d ? x1 >> 16 : x1);
+#pragma unroll
+                                for (int mt = 0; mt < MT; ++mt) mma16816(o[mt][4 * w + 2 * hi + d], pa[mt], b0, b1);
+                            }
+                        }
+                    }
+                } else {
+                    // row by row: the other rows' weights and the tokens the row does not see are zero
+                    for (int rr = 0; rr < rows; ++rr) {
+                        const int rv = SPARSE ? sg.len : sg.len - sg.n + (row0 + rr) / g + 1;
+                        const bool on = !SPARSE || ((pm.mask >> rr) & 1u);
+                        const int mine_mt = rr >> 4, mine_hf = (rr >> 3) & 1;
+                        const bool own = (rr & 7) == i;
+                        uint32_t a[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t x = pa[0][e];
+                            if (MT > 1 && mine_mt == 1) x = pa[MT - 1][e];
+                            a[e] = own && (e & 1) == mine_hf ? x : 0u;
+                        }
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            uint32_t z[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                z[e] = on && pos + 2 * q4 + (e & 1) + 8 * (e >> 1) < rv ? v[e][w] : 0u;
+#pragma unroll
+                            for (int d = 0; d < 4; ++d) {
+                                const uint32_t x0 = __byte_perm(z[0], z[1], d < 2 ? 0x5140 : 0x7362);
+                                const uint32_t x1 = __byte_perm(z[2], z[3], d < 2 ? 0x5140 : 0x7362);
+                                float t[4] = {0.f, 0.f, 0.f, 0.f};
+                                mma16816(t, a, cvt_e4m3x2(d & 1 ? x0 >> 16 : x0), cvt_e4m3x2(d & 1 ? x1 >> 16 : x1));
+#pragma unroll
+                                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e)
+                                        if (own && mt == mine_mt && (e >> 1) == mine_hf) o[mt][4 * w + d][e] += t[e];
+                            }
+                        }
+                    }
+                }
+            } else if (WEIGHTS) {
+                // a page that no row reads (a bad page): zero mass
+                for (int rr = lane; rr < rows && pos < vis_any; rr += 32) {
+                    const size_t rowsw = (size_t)p.max_q * g;
+                    p.ws_mass[((size_t)sg.p0 * p.c.Hkv + (size_t)sg.h * sg.np) * (T / 16) * rowsw +
+                              (size_t)(pos / 16) * rowsw + (SPARSE ? (sg.q0 - p.q_ptr[sg.r]) * g : row0) + rr] =
+                        make_float2(0.f, 0.f);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty0 + 8 * slot);
+        }
+
+        // ---- the four warps' results, joined
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                l[mt][hf] += __shfl_xor_sync(0xffffffffu, l[mt][hf], 1);
+                l[mt][hf] += __shfl_xor_sync(0xffffffffu, l[mt][hf], 2);
+                if (q4 == 0) s_ml[warp * RT + 16 * mt + 8 * hf + i] = make_float2(m[mt][hf], l[mt][hf]);
+            }
+        bar_sync(1, 32 * kConsumers);
+#pragma unroll 1
+        for (int w = 0; w < kConsumers; ++w) {
+            if (warp == w) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const int rr = 16 * mt + 8 * hf + i;
+                        float M = kNegInf;
+#pragma unroll
+                        for (int x = 0; x < kConsumers; ++x) M = fmaxf(M, s_ml[x * RT + rr].x);
+                        const float f = m[mt][hf] == kNegInf ? 0.f : ex2(m[mt][hf] - M);
+                        // d = 16 (2 q4 + e) + j: 16 consecutive floats, stored as four float4 in an order
+                        // that spreads the lanes of a row over the banks
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                float4* dst = reinterpret_cast<float4*>(s_out + rr * kHeadDim + 16 * (2 * q4 + e)) + j;
+                                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                                if (w > 0) x = *dst;
+                                const float a0 = o[mt][4 * j][2 * hf + e], a1 = o[mt][4 * j + 1][2 * hf + e],
+                                            a2 = o[mt][4 * j + 2][2 * hf + e], a3 = o[mt][4 * j + 3][2 * hf + e];
+                                // a warp that saw nothing adds nothing (its factor 0 times 0)
+                                *dst = make_float4(x.x + a0 * f, x.y + a1 * f, x.z + a2 * f, x.w + a3 * f);
+                            }
+                    }
+            }
+            bar_sync(1, 32 * kConsumers);
+        }
+        if (!dead) {
+            // complete: this CTA saw all of the item's units; else a partial result
+            const bool complete = SPARSE ? p.nsplit == 1 : (sg.b0 == 0 && sg.b1 >= sg.nvis);
+            const size_t part = SPARSE ? (size_t)blockIdx.x : (size_t)2 * blockIdx.x + (first_seg ? 0 : 1);
+            for (int rr = warp; rr < rows; rr += kConsumers) {
+                float M = kNegInf, Ls = 0.f;
+#pragma unroll
+                for (int x = 0; x < kConsumers; ++x) M = fmaxf(M, s_ml[x * RT + rr].x);
+#pragma unroll
+                for (int x = 0; x < kConsumers; ++x) {
+                    const float2 a = s_ml[x * RT + rr];
+                    Ls += a.x == kNegInf ? a.y : a.y * ex2(a.x - M);
+                }
+                float4 v = *reinterpret_cast<const float4*>(s_out + rr * kHeadDim + 4 * lane);
+                if (complete) {
+                    const float inv = Ls == 0.f ? 0.f : __fdividef(1.f, Ls);
+                    const int x = row0 + rr, qi = SPARSE ? 0 : x / g, j = x - qi * g;
+                    const size_t at = (size_t)(sg.q0 + qi) * p.Hq + sg.h * g + j;
+                    uint2 w;
+                    w.x = pack_bf16x2(v.x * inv, v.y * inv);
+                    w.y = pack_bf16x2(v.z * inv, v.w * inv);
+                    reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.O) + at * kHeadDim)[lane] = w;
+                    const float l2 = Ls == 0.f ? kNegInf : M - kOffset + lg2(Ls);
+                    if (lane == 0 && p.lse) p.lse[at] = l2 * 0.69314718055994531f;
+                    if (WEIGHTS && lane == 0) p.ws_lse[at] = l2;
+                } else if (!SPARSE ? e0 < e1 : true) {
+                    float* dst = p.part_o + (part * RT + rr) * kHeadDim;
+                    reinterpret_cast<float4*>(dst)[lane] = v;
+                    if (lane == 0) p.part_ml[part * RT + rr] = make_float2(M, Ls);
+                }
+            }
+        }
+        bar_sync(1, 32 * kConsumers);  // s_out and s_ml are free again
+        first_seg = false;
+    }
+}
+
+// ------------------------------------------------------------------ merge
+__device__ __forceinline__ void merge_write(const CacheAttnParams& p, int q0, int h, int x, float M, float Ls, float4 v,
+                                            int lane) {
+    const int qi = x / p.g, j = x - qi * p.g;
+    const size_t at = (size_t)(q0 + qi) * p.Hq + h * p.g + j;
+    const float inv = Ls == 0.f ? 0.f : __fdividef(1.f, Ls);
+    uint2 w;
+    w.x = pack_bf16x2(v.x * inv, v.y * inv);
+    w.y = pack_bf16x2(v.z * inv, v.w * inv);
+    reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.O) + at * kHeadDim)[lane] = w;
+    if (lane == 0) {
+        const float l2 = Ls == 0.f ? kNegInf : M - kOffset + lg2(Ls);
+        if (p.lse) p.lse[at] = l2 * 0.69314718055994531f;
+        if (p.weight) p.ws_lse[at] = l2;
+    }
+}
+
+// One CTA per item: the partial results of its rows, in the order of the CTAs that left them.  Rows
+// of an item that one CTA finished are left alone; rows that see nothing get O = 0, lse = -inf.
+template <int RT, bool SPARSE>
+__global__ void __launch_bounds__(kHeadDim) cache_merge_kernel(const __grid_constant__ CacheAttnParams p, int grid_x) {
+    __shared__ long long red[2][kHeadDim / 32];
+    grid_dep_wait();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = p.g;
+    int q0, rows, row0, h, c0, nc;
+    if constexpr (SPARSE) {
+        const int item = blockIdx.x;
+        q0 = item / p.c.Hkv;
+        h = item - q0 * p.c.Hkv;
+        row0 = 0;
+        rows = g;
+        c0 = item * p.nsplit;
+        nc = p.nsplit;
+        bool in = false;
+        for (int r = tid; r < p.c.R; r += kHeadDim) in = in || (p.q_ptr[r] <= q0 && q0 < p.q_ptr[r + 1]);
+        if (!__syncthreads_or(in)) return;
+    } else {
+        const int per_r = p.c.Hkv * p.max_tiles, r = blockIdx.x / per_r, x = blockIdx.x - r * per_r;
+        const Request q = load_request(p.q_ptr, p.Nq, p.c.kv_len, p.c.page_ptr, p.c.total_pages, p.c.T, r);
+        const bool rows_ok = q.q0 >= 0 && q.n >= 0 && (long long)q.q0 + q.n <= p.Nq;
+        const bool ok = request_fault(p, q) == 0u;
+        const int nt = rows_ok ? tiles_of(min(q.n, p.max_q), g, RT) : 0;
+        h = x / p.max_tiles;
+        const int tile = x - h * p.max_tiles;
+        if (tile >= nt) return;
+        q0 = q.q0;
+        row0 = tile * RT;
+        rows = min(RT, min(q.n, p.max_q) * g - row0);
+        const int nb = ok ? units_of(q.len) : 0;
+        const int vis = q.len - q.n + (row0 + rows - 1) / g + 1;
+        const int nvis = !ok || vis <= 0 ? 0 : units_of(vis);
+        c0 = 0;
+        nc = 0;
+        if (nvis > 0) {
+            long long sum = 0, upto = 0;
+            unsigned bad = 0;
+            for (int y = tid; y < p.c.R; y += kHeadDim) {
+                const int u = request_units(p, y, RT, &bad);
+                sum += u;
+                if (y < r) upto += u;
+            }
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1) {
+                sum += __shfl_xor_sync(0xffffffffu, sum, s);
+                upto += __shfl_xor_sync(0xffffffffu, upto, s);
+            }
+            if (lane == 0) {
+                red[0][warp] = sum;
+                red[1][warp] = upto;
+            }
+            __syncthreads();
+            sum = upto = 0;
+            for (int y = 0; y < kHeadDim / 32; ++y) {
+                sum += red[0][y];
+                upto += red[1][y];
+            }
+            const int per = units_per_cta(p, sum, grid_x);
+            const long long a = upto + (h * nt + tile) * nb;  // the item's first unit
+            c0 = (int)(a / per);
+            nc = (int)((a + nvis - 1) / per) - c0 + 1;
+            if (nc == 1) return;
+            // CTA c's partial is its first segment's unless the item begins inside its run
+            row0 = tile * RT;
+            for (int rr = warp; rr < rows; rr += kHeadDim / 32) {
+                float M = kNegInf, Ls = 0.f;
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int c = c0; c < c0 + nc; ++c)
+                    M = fmaxf(M, p.part_ml[((size_t)2 * c + ((long long)c * per >= a ? 0 : 1)) * RT + rr].x);
+                for (int c = c0; c < c0 + nc; ++c) {
+                    const size_t at = ((size_t)2 * c + ((long long)c * per >= a ? 0 : 1)) * RT + rr;
+                    const float2 ml = p.part_ml[at];
+                    const float f = ml.x == kNegInf ? (ml.y == 0.f ? 0.f : 1.f) : ex2(ml.x - M);
+                    const float4 v = reinterpret_cast<const float4*>(p.part_o + at * kHeadDim)[lane];
+                    Ls += ml.y * f;
+                    acc.x += v.x * f;
+                    acc.y += v.y * f;
+                    acc.z += v.z * f;
+                    acc.w += v.w * f;
+                }
+                merge_write(p, q0, h, row0 + rr, M, Ls, acc, lane);
+            }
+            return;
+        }
+    }
+    for (int rr = warp; rr < rows; rr += kHeadDim / 32) {
+        float M = kNegInf, Ls = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = c0; c < c0 + nc; ++c) M = fmaxf(M, p.part_ml[(size_t)c * RT + rr].x);
+        for (int c = c0; c < c0 + nc; ++c) {
+            const size_t at = (size_t)c * RT + rr;
+            const float2 ml = p.part_ml[at];
+            const float f = ml.x == kNegInf ? (ml.y == 0.f ? 0.f : 1.f) : ex2(ml.x - M);
+            const float4 v = reinterpret_cast<const float4*>(p.part_o + at * kHeadDim)[lane];
+            Ls += ml.y * f;
+            acc.x += v.x * f;
+            acc.y += v.y * f;
+            acc.z += v.z * f;
+            acc.w += v.w * f;
+        }
+        merge_write(p, q0, h, row0 + rr, M, Ls, acc, lane);
+    }
+}
+
+// ------------------------------------------------------------------ page weights
+// weight[page][h] = sum over the request's rows of the softmax weight on the page's tokens, from the
+// sums that the attention kernel kept for every 16 tokens and row (and the maximum each was
+// relative to).  One warp per (page, KV head); lanes over (16 tokens, row), added in a fixed order.
+constexpr int kWeightWarps = 8;
+template <bool SPARSE>
+__global__ void __launch_bounds__(32 * kWeightWarps) cache_weight_kernel(const __grid_constant__ CacheAttnParams p) {
+    grid_dep_wait();
+    const int lane = threadIdx.x & 31;
+    const long long x = (long long)blockIdx.x * kWeightWarps + (threadIdx.x >> 5);
+    if (x >= (long long)p.c.total_pages * p.c.Hkv) return;
+    const int u = (int)(x / p.c.Hkv), h = (int)(x - (long long)u * p.c.Hkv);
+    int r = -1;
+    for (int y0 = 0; y0 < p.c.R && r < 0; y0 += 32) {
+        const int y = y0 + lane;
+        const bool in = y < p.c.R && p.c.page_ptr[y] <= u && u < p.c.page_ptr[y + 1];
+        const unsigned bal = __ballot_sync(0xffffffffu, in);
+        if (bal) r = y0 + __ffs(bal) - 1;
+    }
+    if (r < 0) return;  // a page of no request: left as it is
+    const Request q = load_request(p.q_ptr, p.Nq, p.c.kv_len, p.c.page_ptr, p.c.total_pages, p.c.T, r);
+    float sum = 0.f;
+    const int T = p.c.T, g = p.g, pg = u - q.p0;
+    if (request_fault(p, q) == 0u) {
+        const size_t rowsw = (size_t)p.max_q * g;
+        const float2* src = p.ws_mass + ((size_t)q.p0 * p.c.Hkv + (size_t)h * q.np) * (T / 16) * rowsw +
+                            (size_t)pg * (T / 16) * rowsw;
+        const int rows = q.n * g, total = rows * (T / 16);
+        const uint32_t* bits = SPARSE ? p.ws_bits + (size_t)(q.p0 / 32 + r) * p.max_q * p.c.Hkv : nullptr;
+        for (int e = lane; e < total; e += 32) {
+            const int grp = e / rows, row = e - grp * rows, qi = row / g, j = row - qi * g;
+            const int pos = pg * T + 16 * grp;
+            // the attention kernel reads whole tiles: what a row does not see it has as zero, but
+            // 16 tokens that no row of its tile sees it leaves out
+            if (pos >= q.len - q.n + qi + 1) continue;
+            if (SPARSE && !((bits[((size_t)qi * p.c.Hkv + h) * ((q.np + 31) / 32) + (pg >> 5)] >> (pg & 31)) & 1u))
+                continue;
+            const float2 a = src[(size_t)grp * rowsw + row];
+            const float l2 = p.ws_lse[(size_t)(q.q0 + qi) * p.Hq + h * g + j];
+            // a row whose running maximum was still -inf has 0 here; NaN stays NaN
+            sum += a.x == 0.f ? 0.f : a.x * ex2((a.y == kNegInf ? 0.f : a.y - kOffset) - l2);
+        }
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+    }
+    if (lane == 0) p.weight[(size_t)u * p.c.Hkv + h] = sum;
+}
+
+template <int MT, bool SPARSE, bool WEIGHTS>
+cudaError_t launch_main(const CUtensorMap& tmK, const CUtensorMap& tmV, const CacheAttnParams& p, int grid,
+                        cudaStream_t stream) {
+    const size_t smem = cache_attn_smem(MT, SPARSE, p.max_pages, p.list_cap);
+    const cudaError_t e = ensure_smem_attr((const void*)cache_attn_kernel<MT, SPARSE, WEIGHTS>, smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(cache_attn_kernel<MT, SPARSE, WEIGHTS>, dim3(grid), dim3(kThreads), smem, stream, tmK, tmV, p);
+}
+
+template <int MT>
+cudaError_t launch_mt(const CUtensorMap& tmK, const CUtensorMap& tmV, const CacheAttnParams& p, int grid, int items,
+                      cudaStream_t stream) {
+    const bool sparse = p.topk != nullptr, weights = p.weight != nullptr;
+    cudaError_t e;
+    if (sparse)
+        e = weights ? launch_main<MT, true, true>(tmK, tmV, p, grid, stream)
+                    : launch_main<MT, true, false>(tmK, tmV, p, grid, stream);
+    else
+        e = weights ? launch_main<MT, false, true>(tmK, tmV, p, grid, stream)
+                    : launch_main<MT, false, false>(tmK, tmV, p, grid, stream);
+    if (e != cudaSuccess) return e;
+    if (!sparse) e = launch_pdl(cache_merge_kernel<16 * MT, false>, dim3(items), dim3(kHeadDim), 0, stream, p, grid);
+    else if (p.nsplit > 1)
+        e = launch_pdl(cache_merge_kernel<16 * MT, true>, dim3(items), dim3(kHeadDim), 0, stream, p, grid);
+    if (e != cudaSuccess || !weights) return e;
+    const long long warps = (long long)p.c.total_pages * p.c.Hkv;
+    const dim3 wgrid((unsigned)((warps + kWeightWarps - 1) / kWeightWarps));
+    return sparse ? launch_pdl(cache_weight_kernel<true>, wgrid, dim3(32 * kWeightWarps), 0, stream, p)
+                  : launch_pdl(cache_weight_kernel<false>, wgrid, dim3(32 * kWeightWarps), 0, stream, p);
+}
+
+}  // namespace
+
+size_t cache_attn_smem(int mt, bool sparse, int max_pages, int list_cap) {
+    size_t s = mt == 1 ? Smem<1>::list : Smem<2>::list;
+    if (sparse) s += (size_t)((max_pages + 31) / 32) * 8 + (size_t)list_cap * 8;
+    return s + 1024;
+}
+
+cudaError_t launch_cache_attn(int mt, const CUtensorMap& tmK, const CUtensorMap& tmV, const CacheAttnParams& p,
+                              int grid, int items, cudaStream_t stream) {
+    return mt == 1 ? launch_mt<1>(tmK, tmV, p, grid, items, stream) : launch_mt<2>(tmK, tmV, p, grid, items, stream);
+}
+
+}  // namespace qup

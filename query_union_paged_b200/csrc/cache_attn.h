@@ -1,0 +1,49 @@
+// cache_attn.h -- parameters and launchers of attention over the 8-bit page-scaled cache
+// (cache_attn.cu), for the C ABI (cache_api.cu).
+#pragma once
+#include <cstddef>
+#include <cstdint>
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "cache.h"
+
+namespace qup {
+
+constexpr int kCacheUnit = 64;       // tokens of a work unit
+constexpr int kCacheMaxCtas = 296;   // CTAs that leave partial results: two on each of 148 SMs
+constexpr int kCacheMaxRows = 32;    // rows of the widest row tile
+
+struct CacheAttnParams {
+    CacheView c;
+    const void* Q;
+    long long q_stride;  // elements between a row's queries
+    const int32_t* q_ptr;
+    const int32_t* topk;  // null: all pages
+    void* O;
+    float* lse;       // or null
+    float* weight;    // page weights, or null
+    float* part_o;    // [partial][row tile][128]: unnormalised sums, and in part_ml the log2 maximum
+    float2* part_ml;  // they are relative to and the sum of weights
+    float2* ws_mass;  // page weights: per (16 tokens, row) the weights' sum and the maximum it is relative to
+    float* ws_lse;    // page weights: log2-domain lse of every row
+    uint32_t* ws_bits;  // page weights over TopK pages: the pages each (query, KV head) reads
+    unsigned* err;
+    unsigned long long wait_limit_ns;
+    float scale_log2;
+    int Nq, max_q, Hq, g, Ksel;
+    int per_units;   // all pages: least units of a CTA
+    int max_tiles;   // all pages: row tiles of max_q queries
+    int nsplit;      // TopK pages: CTAs of one (query, KV head)
+    int max_pages;   // pages of a request, at most
+    int list_cap;    // TopK pages: distinct pages of one CTA, at most
+};
+
+// mt: row tiles of 16 * mt rows (1 or 2)
+size_t cache_attn_smem(int mt, bool sparse, int max_pages, int list_cap);
+// items: (request, KV head, row tile) triples of max_tiles each, or (query, KV head) pairs
+cudaError_t launch_cache_attn(int mt, const CUtensorMap& tmK, const CUtensorMap& tmV, const CacheAttnParams& p,
+                              int grid, int items, cudaStream_t stream);
+
+}  // namespace qup
