@@ -78,8 +78,9 @@ def append(cache, scale, new, page_table, page_ptr, kv_len, tok_ptr):
 
 
 def attn(q, K, V, k_scale, v_scale, page_table, page_ptr, kv_len, q_ptr, softmax_scale, topk=None):
-    """O, lse, page weights, and for error bounds, per (row, head): the largest sum |q||k| of a visible
-    token (scaled), and per element the weighted mean of |v|.  q [N][Hq][D] float64."""
+    """O, lse, page weights, and for error bounds, per (row, head): smag, the largest sum |q||k| of a visible
+    token, qk, the largest max|q| sum|k| (both scaled), vtop, the largest |v|, and per element vmag, the
+    weighted mean of |v|.  q [N][Hq][D] float64."""
     N, Hq, _ = q.shape
     Hkv, T = K.shape[1], K.shape[2]
     g = Hq // Hkv
@@ -89,6 +90,7 @@ def attn(q, K, V, k_scale, v_scale, page_table, page_ptr, kv_len, q_ptr, softmax
     smag = np.zeros((N, Hq))
     vmag = np.zeros((N, Hq, D))
     vtop = np.zeros((N, Hq))
+    qk = np.zeros((N, Hq))
     for r in range(len(kv_len)):
         n, L = q_ptr[r + 1] - q_ptr[r], kv_len[r]
         if n == 0 or L == 0:
@@ -121,7 +123,8 @@ def attn(q, K, V, k_scale, v_scale, page_table, page_ptr, kv_len, q_ptr, softmax
                     smag[row, hq] = (np.abs(k[tok]) @ np.abs(q[row, hq])).max() * softmax_scale
                     vmag[row, hq] = p @ np.abs(v[tok])
                     vtop[row, hq] = np.abs(v[tok]).max()
-    return dict(o=O, lse=lse, weight=weight, smag=smag, vmag=vmag, vtop=vtop)
+                    qk[row, hq] = np.abs(q[row, hq]).max() * np.abs(k[tok]).sum(axis=1).max() * softmax_scale
+    return dict(o=O, lse=lse, weight=weight, smag=smag, vmag=vmag, vtop=vtop, qk=qk)
 
 
 def evict(page_table, acc, weight, page_ptr, kv_len, T, budget, sink, recent, decay):

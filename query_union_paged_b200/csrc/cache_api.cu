@@ -50,7 +50,7 @@ qup::CacheView view_of(const qup_cache* c) {
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct AttnWs {
-    size_t part_o, part_ml, mass, lse, bits, total;
+    size_t part_o, part_ml, chunk_o, chunk_ml, spans, mass, lse, bits, total;
 };
 
 // The partial results of an all-pages call: two of each CTA.  Those of a TopK call: one of each CTA
@@ -63,6 +63,14 @@ AttnWs attn_ws_layout(const qup_cache* c, int Nq, int max_q, int Hq, bool weight
     off = align256(off + parts * qup::kHeadDim * sizeof(float));
     w.part_ml = off;
     off = align256(off + parts * sizeof(float2));
+    const size_t crows = 2 * (size_t)qup::kChunkMaxRuns * qup::kChunkRows;
+    const bool chunks = (int64_t)max_q * (Hq / c->Hkv) > qup::kCacheSmallRows;
+    w.chunk_o = off;
+    if (chunks) off = align256(off + crows * qup::kHeadDim * sizeof(float));
+    w.chunk_ml = off;
+    if (chunks) off = align256(off + crows * sizeof(float2));
+    w.spans = off;
+    if (chunks) off = align256(off + qup::kChunkMaxRuns * sizeof(qup::ChunkSpan));
     w.mass = w.lse = w.bits = off;
     if (weights) {
         off = align256(off + sizeof(float2) * (size_t)c->total_pages * (c->T / 16) * Hq * max_q);
@@ -140,10 +148,17 @@ int qup_cache_attn(const qup_cache* cache, const void* Q, int64_t q_stride, cons
     const AttnWs L = attn_ws_layout(cache, Nq, max_q, Hq, page_weight != nullptr);
     if (ws_bytes < L.total) return QUP_ERR_CAPACITY;
 
-    const int mt = (sparse ? g : max_q * g) <= 16 ? 1 : 2, rt = 16 * mt;
+    // All pages: requests of up to kCacheSmallRows rows (queries x heads of a KV head) go to the kernel
+    // of the small ones, the others to the chunk kernel.  Where every request has max_q queries or
+    // the batch is padded, one kernel takes them all.
+    const int64_t big = (int64_t)max_q * g;
+    const bool chunk = !sparse && big > qup::kCacheSmallRows;
+    const bool small = !chunk || (int64_t)c.R * max_q != Nq;
+    const int mt = sparse && g > 16 ? 2 : 1, rt = 16 * mt;
     qup::CacheAttnParams p;
     std::memset(&p, 0, sizeof(p));
-    p.max_tiles = (max_q * g + rt - 1) / rt;
+    p.big_rows = !chunk ? 0x7fffffff : (small ? qup::kCacheSmallRows + 1 : 1);
+    p.max_tiles = (int)((std::min<int64_t>(big, chunk ? qup::kCacheSmallRows : big) + rt - 1) / rt);
     const int64_t max_units = ((int64_t)c.max_pages * c.T + qup::kCacheUnit - 1) / qup::kCacheUnit;
     if (!sparse && (int64_t)p.max_tiles * c.Hkv * max_units >= ((int64_t)1 << 31)) return QUP_ERR_ARG;
     const int64_t items = sparse ? (int64_t)Nq * c.Hkv : (int64_t)c.R * c.Hkv * p.max_tiles;
@@ -161,21 +176,27 @@ int qup_cache_attn(const qup_cache* cache, const void* Q, int64_t q_stride, cons
         p.list_cap = (int)((entries + p.nsplit - 1) / p.nsplit);
         grid = (int)(items * p.nsplit);
     }
-    if (qup::cache_attn_smem(mt, sparse, c.max_pages, p.list_cap) > (size_t)dev.smem_optin) return QUP_ERR_ARG;
+    if (qup::cache_attn_smem(mt, sparse, c.max_pages, p.list_cap) > (size_t)dev.smem_optin ||
+        qup::cache_chunk_smem() > (size_t)dev.smem_optin)
+        return QUP_ERR_ARG;
 
-    // K and V tiles: dims (d, T, Hkv, P_phys) bytes, box (128, min(T, unit), 1, 1), 128-byte swizzle
-    CUtensorMap tm[2];
-    const cuuint64_t row = qup::kHeadDim, page = row * c.T;
-    const cuuint64_t dims[4] = {row, (cuuint64_t)c.T, (cuuint64_t)c.Hkv, (cuuint64_t)c.P_phys};
-    const cuuint64_t strides[3] = {row, page, page * c.Hkv};
-    const cuuint32_t box[4] = {(cuuint32_t)qup::kHeadDim, (cuuint32_t)std::min(c.T, qup::kCacheUnit), 1, 1};
-    const cuuint32_t estr[4] = {1, 1, 1, 1};
-    void* const srcs[2] = {c.K, c.V};
-    for (int i = 0; i < 2; ++i)
-        if (dev.encode(&tm[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, srcs[i], dims, strides, box, estr,
-                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-            return QUP_ERR_ARG;
+    // K and V tiles: dims (d, T, Hkv, P_phys) bytes, boxes of (128, tokens, 1, 1), 128-byte swizzle
+    const auto encode = [&](int box_tokens, CUtensorMap* tm) {
+        const cuuint64_t row = qup::kHeadDim, page = row * c.T;
+        const cuuint64_t dims[4] = {row, (cuuint64_t)c.T, (cuuint64_t)c.Hkv, (cuuint64_t)c.P_phys};
+        const cuuint64_t strides[3] = {row, page, page * c.Hkv};
+        const cuuint32_t box[4] = {(cuuint32_t)qup::kHeadDim, (cuuint32_t)box_tokens, 1, 1};
+        const cuuint32_t estr[4] = {1, 1, 1, 1};
+        void* const srcs[2] = {c.K, c.V};
+        for (int i = 0; i < 2; ++i)
+            if (dev.encode(&tm[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, srcs[i], dims, strides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+                return false;
+        return true;
+    };
+    CUtensorMap tm[2], tmc[2];
+    if ((small && !encode(std::min(c.T, qup::kCacheUnit), tm)) || (chunk && !encode(c.T, tmc))) return QUP_ERR_ARG;
 
     char* base = static_cast<char*>(ws);
     p.c = view_of(cache);
@@ -188,6 +209,9 @@ int qup_cache_attn(const qup_cache* cache, const void* Q, int64_t q_stride, cons
     p.weight = page_weight;
     p.part_o = reinterpret_cast<float*>(base + L.part_o);
     p.part_ml = reinterpret_cast<float2*>(base + L.part_ml);
+    p.chunk_o = reinterpret_cast<float*>(base + L.chunk_o);
+    p.chunk_ml = reinterpret_cast<float2*>(base + L.chunk_ml);
+    p.spans = reinterpret_cast<qup::ChunkSpan*>(base + L.spans);
     p.ws_mass = reinterpret_cast<float2*>(base + L.mass);
     p.ws_lse = reinterpret_cast<float*>(base + L.lse);
     p.ws_bits = reinterpret_cast<uint32_t*>(base + L.bits);
@@ -201,10 +225,12 @@ int qup_cache_attn(const qup_cache* cache, const void* Q, int64_t q_stride, cons
     p.Ksel = Ksel;
     p.per_units = 1;
     p.max_pages = c.max_pages;
-    return qup::launch_cache_attn(mt, tm[0], tm[1], p, grid, (int)items, static_cast<cudaStream_t>(stream)) ==
-                   cudaSuccess
-               ? QUP_OK
-               : QUP_ERR_CUDA;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (chunk && qup::launch_cache_chunk(tmc[0], tmc[1], p, std::min(dev.sms, qup::kChunkMaxRuns), st) != cudaSuccess)
+        return QUP_ERR_CUDA;
+    if (small && qup::launch_cache_attn(mt, tm[0], tm[1], p, grid, (int)items, st) != cudaSuccess) return QUP_ERR_CUDA;
+    if (page_weight && qup::launch_cache_weights(p, st) != cudaSuccess) return QUP_ERR_CUDA;
+    return QUP_OK;
 }
 
 int qup_cache_evict(const qup_cache* cache, const float* page_weight, const float* acc, float decay, int budget,

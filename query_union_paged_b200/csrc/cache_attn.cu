@@ -108,6 +108,7 @@ __device__ __forceinline__ unsigned request_fault(const CacheAttnParams& p, cons
 }
 __device__ __forceinline__ int request_units(const CacheAttnParams& p, int r, int RT, unsigned* bad) {
     const Request q = load_request(p.q_ptr, p.Nq, p.c.kv_len, p.c.page_ptr, p.c.total_pages, p.c.T, r);
+    if ((long long)q.n * p.g >= p.big_rows) return 0;  // the chunk kernel's
     const unsigned f = request_fault(p, q);
     *bad |= f;
     return f ? 0 : tiles_of(q.n, p.g, RT) * p.c.Hkv * units_of(q.len);
@@ -145,7 +146,7 @@ struct Cursor {
             if (nb < 0) {
                 if (r >= p.c.R) return false;
                 q = load_request(p.q_ptr, p.Nq, p.c.kv_len, p.c.page_ptr, p.c.total_pages, p.c.T, r);
-                const bool ok = request_fault(p, q) == 0u;
+                const bool ok = request_fault(p, q) == 0u && (long long)q.n * p.g < p.big_rows;
                 nb = ok ? units_of(q.len) : 0;
                 nt = ok ? tiles_of(q.n, p.g, RT) : 0;
             }
@@ -810,7 +811,8 @@ __global__ void __launch_bounds__(kHeadDim) cache_merge_kernel(const __grid_cons
     } else {
         const int per_r = p.c.Hkv * p.max_tiles, r = blockIdx.x / per_r, x = blockIdx.x - r * per_r;
         const Request q = load_request(p.q_ptr, p.Nq, p.c.kv_len, p.c.page_ptr, p.c.total_pages, p.c.T, r);
-        const bool rows_ok = q.q0 >= 0 && q.n >= 0 && (long long)q.q0 + q.n <= p.Nq;
+        const bool rows_ok =
+            q.q0 >= 0 && q.n >= 0 && (long long)q.q0 + q.n <= p.Nq && (long long)q.n * g < p.big_rows;
         const bool ok = request_fault(p, q) == 0u;
         const int nt = rows_ok ? tiles_of(min(q.n, p.max_q), g, RT) : 0;
         h = x / p.max_tiles;
@@ -921,7 +923,8 @@ __global__ void __launch_bounds__(32 * kWeightWarps) cache_weight_kernel(const _
         const size_t rowsw = (size_t)p.max_q * g;
         const float2* src = p.ws_mass + ((size_t)q.p0 * p.c.Hkv + (size_t)h * q.np) * (T / 16) * rowsw +
                             (size_t)pg * (T / 16) * rowsw;
-        const int rows = q.n * g, total = rows * (T / 16);
+        // the chunk kernel keeps one sum for each page and row, in the place of its first 16 tokens
+        const int rows = q.n * g, total = rows * (!SPARSE && rows >= p.big_rows ? 1 : T / 16);
         const uint32_t* bits = SPARSE ? p.ws_bits + (size_t)(q.p0 / 32 + r) * p.max_q * p.c.Hkv : nullptr;
         for (int e = lane; e < total; e += 32) {
             const int grp = e / rows, row = e - grp * rows, qi = row / g, j = row - qi * g;
@@ -966,11 +969,7 @@ cudaError_t launch_mt(const CUtensorMap& tmK, const CUtensorMap& tmV, const Cach
     if (!sparse) e = launch_pdl(cache_merge_kernel<16 * MT, false>, dim3(items), dim3(kHeadDim), 0, stream, p, grid);
     else if (p.nsplit > 1)
         e = launch_pdl(cache_merge_kernel<16 * MT, true>, dim3(items), dim3(kHeadDim), 0, stream, p, grid);
-    if (e != cudaSuccess || !weights) return e;
-    const long long warps = (long long)p.c.total_pages * p.c.Hkv;
-    const dim3 wgrid((unsigned)((warps + kWeightWarps - 1) / kWeightWarps));
-    return sparse ? launch_pdl(cache_weight_kernel<true>, wgrid, dim3(32 * kWeightWarps), 0, stream, p)
-                  : launch_pdl(cache_weight_kernel<false>, wgrid, dim3(32 * kWeightWarps), 0, stream, p);
+    return e;
 }
 
 }  // namespace
@@ -984,6 +983,13 @@ size_t cache_attn_smem(int mt, bool sparse, int max_pages, int list_cap) {
 cudaError_t launch_cache_attn(int mt, const CUtensorMap& tmK, const CUtensorMap& tmV, const CacheAttnParams& p,
                               int grid, int items, cudaStream_t stream) {
     return mt == 1 ? launch_mt<1>(tmK, tmV, p, grid, items, stream) : launch_mt<2>(tmK, tmV, p, grid, items, stream);
+}
+
+cudaError_t launch_cache_weights(const CacheAttnParams& p, cudaStream_t stream) {
+    const long long warps = (long long)p.c.total_pages * p.c.Hkv;
+    const dim3 grid((unsigned)((warps + kWeightWarps - 1) / kWeightWarps));
+    return p.topk ? launch_pdl(cache_weight_kernel<true>, grid, dim3(32 * kWeightWarps), 0, stream, p)
+                  : launch_pdl(cache_weight_kernel<false>, grid, dim3(32 * kWeightWarps), 0, stream, p);
 }
 
 }  // namespace qup

@@ -14,6 +14,16 @@ namespace qup {
 constexpr int kCacheUnit = 64;       // tokens of a work unit
 constexpr int kCacheMaxCtas = 296;   // CTAs that leave partial results: two on each of 148 SMs
 constexpr int kCacheMaxRows = 32;    // rows of the widest row tile
+constexpr int kCacheSmallRows = 16;  // rows (queries x heads of a KV head) up to which a request is a small one
+constexpr int kChunkRows = 256;      // rows of an item of the other kernel (cache_chunk.cu)
+constexpr int kChunkMaxRuns = 148;   // and its CTAs
+
+// What a CTA of the chunk kernel worked on: its last item, from which step, whether the item ends
+// with it, and the first item's end.
+struct ChunkSpan {
+    int r, h, tile, b0;
+    int ends, first_ends, segs, pad;
+};
 
 struct CacheAttnParams {
     CacheView c;
@@ -29,6 +39,9 @@ struct CacheAttnParams {
     float2* ws_mass;  // page weights: per (16 tokens, row) the weights' sum and the maximum it is relative to
     float* ws_lse;    // page weights: log2-domain lse of every row
     uint32_t* ws_bits;  // page weights over TopK pages: the pages each (query, KV head) reads
+    float* chunk_o;     // [2 per run][256][128], chunk_ml, spans [run]: the chunk kernel's partial results
+    float2* chunk_ml;
+    ChunkSpan* spans;
     unsigned* err;
     unsigned long long wait_limit_ns;
     float scale_log2;
@@ -37,6 +50,7 @@ struct CacheAttnParams {
     int max_tiles;   // all pages: row tiles of max_q queries
     int nsplit;      // TopK pages: CTAs of one (query, KV head)
     int max_pages;   // pages of a request, at most
+    int big_rows;    // all pages: requests of this many rows or more are the chunk kernel's
     int list_cap;    // TopK pages: distinct pages of one CTA, at most
 };
 
@@ -45,5 +59,11 @@ size_t cache_attn_smem(int mt, bool sparse, int max_pages, int list_cap);
 // items: (request, KV head, row tile) triples of max_tiles each, or (query, KV head) pairs
 cudaError_t launch_cache_attn(int mt, const CUtensorMap& tmK, const CUtensorMap& tmV, const CacheAttnParams& p,
                               int grid, int items, cudaStream_t stream);
+// the requests of big_rows or more; tensor maps with boxes of a whole page
+size_t cache_chunk_smem();
+cudaError_t launch_cache_chunk(const CUtensorMap& tmK, const CUtensorMap& tmV, const CacheAttnParams& p, int runs,
+                               cudaStream_t stream);
+// page weights from what the attention kernels left
+cudaError_t launch_cache_weights(const CacheAttnParams& p, cudaStream_t stream);
 
 }  // namespace qup

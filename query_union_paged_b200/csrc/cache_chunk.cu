@@ -1,0 +1,902 @@
+// cache_chunk.cu -- attention over the 8-bit page-scaled cache for requests with many query rows
+// (chunks of a prompt, drafted tokens): tcgen05 with the accumulators in TMEM.
+//
+// The mathematics is cache_attn.cu's: per row x_t = f q.k_t + log2 vs, with f = softmax_scale * log2e *
+// ks of the token's page, p_t = 2^(x_t - m + 8), O = sum p_t v_t / sum (p_t / vs).
+//
+// Numbers.  S = Q K^T runs in kind::f8f6f4 straight on the cache's bytes: a bf16 row of Q is the sum of
+// two E4M3 rows.  With the row scaled by a power of two so that its largest element lies in [128, 256),
+// the high part is that element rounded to E4M3 (4 significant bits) and the low part the rest (at
+// most 4 bits): exact for elements down to 2^-9 of the largest, within 2^-17 of the largest below.
+// Two products of 8-bit operands cost what one of 16-bit operands does, and K needs no conversion.
+// fp32 sums of E4M3 products on this part were measured against fp64: within 2^-21 of sum |q||k|.
+// P is rounded to fp16 (half step 2^-11), V converted to fp16 (exact), O and the row sums are fp32.
+//
+// A work item is a tile of 256 rows (query, head of the KV head's group) of one KV head: two row tiles
+// of 128, each with a softmax warpgroup, an S buffer and an O accumulator (512 TMEM columns).  While one
+// warpgroup computes exponentials the tensor cores work for the other.  Steps of 128 tokens: all items'
+// visible steps are laid end to end and cut into one equal run per CTA (one per SM); an item cut by a
+// run's end leaves partial results, which a second kernel joins in a fixed order.
+//
+// Warps (384 threads): 0-3 and 4-7 softmax of row tile 0 and 1 (thread = row); 8 loads the K and V bytes
+// by TMA two steps ahead and issues S; 9 issues O += P V; 10 and 11 convert V tiles to fp16 in the
+// 128-byte-swizzled MN-major operand layout.  P goes over S in TMEM.  The loads share a warp with S at
+// no loss: what a load waits for (S of an earlier step, a converted V tile) the next S waits for too.
+//
+// NaN: a NaN byte of V that a row does not see must not reach it as 0 * NaN.  The converters store 0 for
+// it and remember its column's first such token; the epilogue gives NaN to the rows that see it.
+//
+// Bound by the tensor cores and the exponentials: 4 * rows * tokens * 128 flops.
+#include <algorithm>
+#include <cstdint>
+
+#include "cache.h"
+#include "cache_attn.h"
+#include "internal.h"
+#include "ptx.cuh"
+#include "query_union_paged.h"
+
+namespace qup {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kStep = 128;                  // tokens of a step
+constexpr int kTileRows = 128;              // rows of a warpgroup
+constexpr int kItemRows = kChunkRows;       // rows of an item
+constexpr int kTile = kStep * kHeadDim;     // bytes of a K or V tile
+constexpr int kNK = 3, kNV = 2, kNM = 8;    // K tiles, V tiles, page constants in flight
+constexpr int kMarks = 5;                   // segments whose NaN marks are held
+constexpr int kMaxPages = kStep / 16;
+constexpr int kSWarp = 8, kPvWarp = 9, kConvWarp = 10, kConvWarps = 2;
+constexpr int kAhead = 2;                   // steps that the loads are ahead of S
+// registers: the launch gives 384 x 168; the softmax warpgroups take 208 each, the others keep 88
+constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
+static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "register split");
+constexpr uint32_t kColO = 0, kColS = 256;
+constexpr float kOffset = 8.f;     // log2 offset of P
+constexpr float kLazy = 7.f;       // the maximum moves once a score passes it by this: P <= 2^15
+constexpr float kZeroScaleLog2 = -64.f;
+constexpr float kNegInf = -INFINITY;
+
+struct StepMeta {  // the pages of a step
+    float ks[kMaxPages], vl[kMaxPages], vi[kMaxPages];
+    uint32_t valid;
+    uint32_t pad[7];
+};
+
+struct NanMarks {  // of one segment
+    int first[kHeadDim];  // token of the first NaN in each column of V
+    int any;
+    int pad[3];
+};
+
+struct Layout {
+    static constexpr uint32_t q = 0;                                // [2][hi, lo][128][128]
+    static constexpr uint32_t k = q + 4 * kTile;                    // [kNK]
+    static constexpr uint32_t v = k + kNK * kTile;                  // [kNV]
+    static constexpr uint32_t v16 = v + kNV * kTile;                // [2] fp16 tiles
+    static constexpr uint32_t meta = v16 + 4 * kTile;
+    static constexpr uint32_t nan = meta + kNM * sizeof(StepMeta);  // [kMarks]
+    static constexpr uint32_t bars = nan + kMarks * sizeof(NanMarks);
+    static constexpr uint32_t scan = bars + 8 * 40;                 // [kThreads] int64
+    static constexpr uint32_t misc = scan + 8 * kThreads;
+    static constexpr uint32_t total = misc + 64;
+};
+
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t cvt_e4m3x2(uint32_t v) {  // low 16 bits
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)v));
+    return r;
+}
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {  // 0x80 at each E4M3 NaN (0x7f, 0xff)
+    return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+
+// sum over t in [0, n) of floor((a t + b) / m), all non-negative
+__device__ long long floor_sum(long long n, long long m, long long a, long long b) {
+    long long s = 0;
+    while (n > 0) {
+        s += (n - 1) * n / 2 * (a / m) + n * (b / m);
+        a %= m;
+        b %= m;
+        const long long y = a * n + b;
+        if (y < m) break;
+        n = y / m;
+        b = y % m;
+        const long long x = m;
+        m = a;
+        a = x;
+    }
+    return s;
+}
+
+// One request's items.  Row tile t's steps: floor((g (base + 127) + last row) / (128 g)) with base =
+// tokens its first query sees, which is ceil(tokens its last row sees / 128).
+struct Items {
+    Request q;
+    int nt, rows, base;
+    bool ok;
+    __device__ __forceinline__ void load(const CacheAttnParams& p, int r, unsigned* fault) {
+        q = load_request(p.q_ptr, p.Nq, p.c.kv_len, p.c.page_ptr, p.c.total_pages, p.c.T, r);
+        unsigned f = !q.ok || q.n > p.max_q ? QUP_ERR_GROUP : 0u;
+        if (!f && q.np > p.max_pages) f = QUP_ERR_CAPACITY;
+        *fault |= f;
+        ok = f == 0u;
+        const bool rows_ok = q.q0 >= 0 && q.n > 0 && (long long)q.q0 + q.n <= p.Nq;
+        rows = rows_ok ? min(q.n, p.max_q) * p.g : 0;
+        if (rows < p.big_rows) rows = 0;  // the other kernel's
+        nt = (rows + kItemRows - 1) / kItemRows;
+        base = ok ? max(q.len - q.n, 0) + 1 : 0;
+    }
+    __device__ __forceinline__ int steps(const CacheAttnParams& p, int t) const {
+        if (!ok) return 1;
+        const int last = min((t + 1) * kItemRows, rows) - 1;
+        return (int)(((long long)p.g * (base + kStep - 1) + last) / ((long long)kStep * p.g));
+    }
+    // steps of the first t < nt row tiles
+    __device__ __forceinline__ long long before(const CacheAttnParams& p, int t) const {
+        if (!ok) return t;
+        return floor_sum(t, (long long)kStep * p.g, kItemRows, (long long)p.g * (base + kStep - 1) + kItemRows - 1);
+    }
+    __device__ __forceinline__ long long total(const CacheAttnParams& p) const {
+        return nt == 0 ? 0 : (before(p, nt - 1) + steps(p, nt - 1)) * p.c.Hkv;
+    }
+};
+
+struct Seg {
+    int r, h, tile, b0, b1, steps;
+};
+
+struct Walk {  // a CTA's run of steps, item by item
+    int r, h, tile, b, left;
+    bool loaded;
+    Items it;
+    __device__ __forceinline__ void begin(const int* start) {
+        r = start[0];
+        h = start[1];
+        tile = start[2];
+        b = start[3];
+        left = start[4];
+        loaded = false;
+    }
+    __device__ __forceinline__ bool next(const CacheAttnParams& p, Seg& s) {
+        while (left > 0 && r < p.c.R) {
+            if (!loaded) {
+                unsigned f = 0;
+                it.load(p, r, &f);
+                loaded = true;
+            }
+            if (it.nt == 0 || h >= p.c.Hkv) {
+                ++r;
+                h = tile = b = 0;
+                loaded = false;
+                continue;
+            }
+            s.r = r;
+            s.h = h;
+            s.tile = tile;
+            s.steps = it.steps(p, tile);
+            s.b0 = b;
+            s.b1 = min(s.steps, b + left);
+            left -= s.b1 - s.b0;
+            b = s.b1;
+            if (b >= s.steps) {
+                b = 0;
+                if (++tile == it.nt) {
+                    tile = 0;
+                    ++h;
+                }
+            }
+            return true;
+        }
+        return false;
+    }
+};
+
+struct Bars {
+    uint32_t base;
+    __device__ __forceinline__ uint32_t at(int i) const { return base + 8u * i; }
+    __device__ __forceinline__ uint32_t kfull(int s) const { return at(s); }
+    __device__ __forceinline__ uint32_t kempty(int s) const { return at(kNK + s); }
+    __device__ __forceinline__ uint32_t vfull(int s) const { return at(2 * kNK + s); }
+    __device__ __forceinline__ uint32_t vempty(int s) const { return at(2 * kNK + kNV + s); }
+    __device__ __forceinline__ uint32_t f(int i) const { return at(2 * kNK + 2 * kNV + i); }
+    __device__ __forceinline__ uint32_t cfull(int s) const { return f(s); }       // fp16 V written
+    __device__ __forceinline__ uint32_t cempty(int s) const { return f(2 + s); }  // fp16 V read
+    __device__ __forceinline__ uint32_t sfull(int w) const { return f(4 + w); }
+    __device__ __forceinline__ uint32_t pfull(int w) const { return f(6 + w); }
+    __device__ __forceinline__ uint32_t pvdone(int w) const { return f(8 + w); }
+    __device__ __forceinline__ uint32_t qfull(int w) const { return f(10 + w); }
+    __device__ __forceinline__ uint32_t drain(int i) const { return f(12 + i); }
+    __device__ __forceinline__ uint32_t sdone() const { return f(14); }  // every S of a segment issued
+    __device__ __forceinline__ uint32_t mfull(int s) const { return f(15 + s); }
+};
+static_assert(2 * kNK + 2 * kNV + 15 + kNM <= 40, "barrier block");
+
+__device__ __forceinline__ bool warp_ok(bool ok) { return __all_sync(0xffffffffu, ok); }
+
+template <int T, bool WEIGHTS>
+__global__ void __launch_bounds__(kThreads, 1)
+    cache_chunk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                       const __grid_constant__ CacheAttnParams p) {
+    constexpr int PPS = kStep / T;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const Bars B{sbase + Layout::bars};
+    volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + Layout::misc);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Layout::misc + 4);
+    int* s_start = reinterpret_cast<int*>(smem + Layout::misc + 16);  // r, h, tile, b, count
+    long long* scan = reinterpret_cast<long long*>(smem + Layout::scan);
+    StepMeta* meta = reinterpret_cast<StepMeta*>(smem + Layout::meta);
+    NanMarks* marks = reinterpret_cast<NanMarks*>(smem + Layout::nan);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint64_t lim = p.wait_limit_ns;
+    const int g = p.g;
+
+    if (tid == 0) {
+        for (int s = 0; s < kNK; ++s) {
+            mbar_init(B.kfull(s), 1);
+            mbar_init(B.kempty(s), 1);
+        }
+        for (int s = 0; s < kNV; ++s) {
+            mbar_init(B.vfull(s), 1);
+            mbar_init(B.vempty(s), kConvWarps);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(B.cfull(s), kConvWarps);
+            mbar_init(B.cempty(s), 1);
+            mbar_init(B.sfull(s), 1);
+            mbar_init(B.pfull(s), 4);
+            mbar_init(B.pvdone(s), 1);
+            mbar_init(B.qfull(s), 4);
+            mbar_init(B.drain(s), 1);
+        }
+        mbar_init(B.sdone(), 1);
+        for (int s = 0; s < kNM; ++s) mbar_init(B.mfull(s), 1);
+        *abort_flag = 0;
+        s_start[0] = p.c.R;
+        s_start[4] = 0;
+        fence_mbar_init();
+    }
+    for (int i = tid; i < kMarks * (int)(sizeof(NanMarks) / 4); i += kThreads)
+        reinterpret_cast<int*>(marks)[i] = i % (int)(sizeof(NanMarks) / 4) < kHeadDim ? 0x7fffffff : 0;
+    if (tid == kSWarp * 32) {
+        prefetch_tensormap(&tmK);
+        prefetch_tensormap(&tmV);
+    }
+    if (warp == kSWarp) {
+        tmem_alloc(smem_u32((const void*)tmem_slot), 512);
+        tmem_relinquish();
+    }
+    grid_dep_wait();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    {  // this CTA's run: requests' steps added up, each thread over its own consecutive requests
+        const int span = (p.c.R + kThreads - 1) / kThreads;
+        const int r0 = min(p.c.R, tid * span), r1 = min(p.c.R, r0 + span);
+        long long sum = 0;
+        unsigned fault = 0;
+        for (int r = r0; r < r1; ++r) {
+            Items it;
+            it.load(p, r, &fault);
+            sum += it.total(p);
+        }
+        if (fault) atomicOr(p.err, fault);
+        scan[tid] = sum;
+        __syncthreads();
+        long long mine = 0, all = 0;
+        const int used = min(kThreads, p.c.R);  // threads past the last request have no steps
+        for (int t = 0; t < used; ++t) {
+            mine += t < tid ? scan[t] : 0;
+            all += scan[t];
+        }
+        const long long per = max((all + gridDim.x - 1) / gridDim.x, 1ll);
+        const long long u0 = (long long)blockIdx.x * per;
+        if (u0 < all && u0 >= mine && u0 < mine + sum) {
+            long long at = mine;
+            for (int r = r0; r < r1; ++r) {
+                Items it;
+                it.load(p, r, &fault);
+                const long long u = it.total(p);
+                if (u0 < at + u) {
+                    const long long head = u / p.c.Hkv, off = u0 - at;
+                    const long long in = off % head;
+                    int lo = 0, hi = it.nt - 1;  // the last tile whose steps start at or before `in`
+                    while (lo < hi) {
+                        const int mid = (lo + hi + 1) / 2;
+                        if (it.before(p, mid) <= in) lo = mid;
+                        else hi = mid - 1;
+                    }
+                    s_start[0] = r;
+                    s_start[1] = (int)(off / head);
+                    s_start[2] = lo;
+                    s_start[3] = (int)(in - it.before(p, lo));
+                    s_start[4] = (int)min(per, all - u0);
+                    break;
+                }
+                at += u;
+            }
+        }
+        __syncthreads();
+    }
+
+    Walk wk;
+    wk.begin(s_start);
+    Seg sg;
+
+    if (warp >= 8) {
+        regs_decrease<kOtherRegs>();
+        if (warp == kSWarp) {
+            // ==================================================== loads and S
+            Walk lead;  // of the loads
+            lead.begin(s_start);
+            Seg ls{};
+            ChunkSpan info{};
+            int lb = 0;         // the next step to load
+            bool more = true;
+            uint32_t loads = 0;
+            int have0 = 0, have1 = 0, phys = -1;  // page table entries that the lanes hold
+            float ks = 0.f, vl = 0.f, vi = 0.f;
+            const auto load_next = [&]() -> bool {  // false: a wait gave up
+                if (!more) return true;
+                if (lb >= ls.b1) {
+                    more = lead.next(p, ls);
+                    if (!more) return true;
+                    info.r = ls.r;
+                    info.h = ls.h;
+                    info.tile = ls.tile;
+                    info.b0 = ls.b0;
+                    info.ends = ls.b1 == ls.steps;
+                    if (info.segs == 0) info.first_ends = info.ends;
+                    ++info.segs;
+                    lb = ls.b0;
+                    have1 = 0;
+                }
+                const int pe = lb * PPS;
+                if (pe + PPS > have1) {
+                    have0 = pe;
+                    have1 = pe + 32;
+                    const int e = pe + lane, last = lead.it.ok ? (lead.it.q.len + T - 1) / T : 0;
+                    phys = -1;
+                    if (e < last) {
+                        phys = p.c.page_table[lead.it.q.p0 + e];
+                        if (phys < 0 || phys >= p.c.P_phys) {
+                            atomicOr(p.err, QUP_ERR_PHYS_PAGE);
+                            phys = -1;
+                        } else {
+                            ks = __ldg(p.c.k_scale + (size_t)phys * p.c.Hkv + ls.h);
+                            const float vs = __ldg(p.c.v_scale + (size_t)phys * p.c.Hkv + ls.h);
+                            if (!(fabsf(ks) < INFINITY) || !(vs >= 0.f && vs < INFINITY)) {
+                                atomicOr(p.err, QUP_ERR_SCALE);
+                                phys = -1;
+                            }
+                            vl = vs > 0.f ? lg2(vs) : kZeroScaleLog2;
+                            vi = vs > 0.f ? __frcp_rn(vs) : 18446744073709551616.f;
+                        }
+                    }
+                    if (phys < 0) ks = vl = vi = 0.f;
+                }
+                const int src = pe - have0;
+                const uint32_t live = (__ballot_sync(0xffffffffu, phys >= 0) >> src) & ((1u << PPS) - 1u);
+                const uint32_t bytes = __popc(live) * T * kHeadDim;
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    const int n = kv ? kNV : kNK;
+                    const uint32_t slot = loads % n, par = (loads / n) & 1;
+                    if (!warp_ok(mbar_wait_idle(kv ? B.vempty(slot) : B.kempty(slot), par ^ 1, abort_flag, p.err,
+                                                QUP_ERR_TIMEOUT, lim)))
+                        return false;
+                    if (kv == 0) {
+                        // the constants' last readers, kNM steps ago, are done: S of a later step has run
+                        StepMeta& m = meta[loads % kNM];
+                        if (lane >= src && lane < src + PPS) {
+                            m.ks[lane - src] = ks;
+                            m.vl[lane - src] = vl;
+                            m.vi[lane - src] = vi;
+                        }
+                        if (lane == 0) m.valid = live;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(B.mfull(loads % kNM));
+                    }
+                    const uint32_t full = kv ? B.vfull(slot) : B.kfull(slot);
+                    if (lane == 0) {
+                        if (bytes) mbar_arrive_expect_tx(full, bytes);
+                        else mbar_arrive(full);
+                    }
+                    __syncwarp();
+                    if (lane >= src && lane < src + PPS && phys >= 0)
+                        tma_load_4d(sbase + (kv ? Layout::v : Layout::k) + slot * kTile +
+                                        (uint32_t)(lane - src) * T * kHeadDim,
+                                    kv ? &tmV : &tmK, full, 0, 0, ls.h, phys);
+                    __syncwarp();
+                }
+                ++loads;
+                ++lb;
+                return true;
+            };
+            constexpr uint32_t idesc = instr_desc(0, 0, 0, kStep, kTileRows);
+            uint32_t it = 0, use[2] = {0, 0}, segs = 0;
+            bool ok = true;
+            for (int a = 0; a < kAhead && ok; ++a) ok = load_next();
+            while (ok && wk.next(p, sg)) {
+                const int nw = min(kItemRows, wk.it.rows - sg.tile * kItemRows) > kTileRows ? 2 : 1;
+                const uint32_t sp = segs++ & 1;
+                if (nw == 1) ok = warp_ok(mbar_wait_idle(B.qfull(1), sp, abort_flag, p.err, QUP_ERR_TIMEOUT, lim));
+                for (int b = sg.b0; b < sg.b1 && ok; ++b, ++it) {
+                    const uint32_t slot = it % kNK;
+                    ok = warp_ok(mbar_wait_idle(B.kfull(slot), (it / kNK) & 1, abort_flag, p.err, QUP_ERR_TIMEOUT, lim));
+                    for (int w = 0; w < nw && ok; ++w) {
+                        const uint32_t k = use[w]++;
+                        // S_w is free once the O update that last read P from it is done
+                        ok = warp_ok((b > sg.b0 ||
+                                      mbar_wait_idle(B.qfull(w), sp, abort_flag, p.err, QUP_ERR_TIMEOUT, lim)) &&
+                                     (k == 0 || mbar_wait_idle(B.pvdone(w), (k - 1) & 1, abort_flag, p.err,
+                                                               QUP_ERR_TIMEOUT, lim)));
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t qd = smem_desc(sbase + Layout::q + w * 2 * kTile, 16, 1024, 2);
+                        const uint64_t kd = smem_desc(sbase + Layout::k + slot * kTile, 16, 1024, 2);
+                        if (elect_one_sync()) {
+#pragma unroll
+                            for (int kk = 0; kk < 8; ++kk)  // the low parts of Q first
+                                tc_mma<2>(tmem + kColS + 128u * w, qd + (((kk < 4 ? kTile : 0) + (kk & 3) * 32) >> 4),
+                                          kd + (((kk & 3) * 32) >> 4), idesc, kk > 0);
+                            tc_commit(B.sfull(w));
+                            if (w == nw - 1) tc_commit(B.kempty(slot));
+                        }
+                        __syncwarp();
+                    }
+                    if (ok) ok = load_next();
+                }
+                if (lane == 0) mbar_arrive(B.sdone());
+                __syncwarp();
+            }
+            if (elect_one_sync()) tc_commit(B.drain(0));
+            __syncwarp();
+            mbar_wait_drain(B.drain(0), 0, lim);
+            if (lane == 0) {
+                p.spans[blockIdx.x] = info;
+                if (*abort_flag) {  // what is in flight lands before the CTA leaves
+                    for (uint32_t k = loads > (uint32_t)kNK ? loads - kNK : 0; k <= loads; ++k)
+                        mbar_wait_drain(B.kfull(k % kNK), (k / kNK) & 1, lim / 16);
+                    for (uint32_t k = loads > (uint32_t)kNV ? loads - kNV : 0; k <= loads; ++k)
+                        mbar_wait_drain(B.vfull(k % kNV), (k / kNV) & 1, lim / 16);
+                }
+            }
+            __syncwarp();
+        } else if (warp == kPvWarp) {
+            // ==================================================== O += P V
+            constexpr uint32_t idesc = instr_desc(0, 0, 1, kHeadDim, kTileRows);
+            uint32_t it = 0, use[2] = {0, 0};
+            bool ok = true;
+            while (ok && wk.next(p, sg)) {
+                const int nw = min(kItemRows, wk.it.rows - sg.tile * kItemRows) > kTileRows ? 2 : 1;
+                for (int b = sg.b0; b < sg.b1 && ok; ++b, ++it) {
+                    const uint32_t slot = it & 1;
+                    ok = warp_ok(mbar_wait_idle(B.cfull(slot), (it >> 1) & 1, abort_flag, p.err, QUP_ERR_TIMEOUT, lim));
+                    for (int w = 0; w < nw && ok; ++w) {
+                        const uint32_t k = use[w]++;
+                        ok = warp_ok(mbar_wait_idle(B.pfull(w), k & 1, abort_flag, p.err, QUP_ERR_TIMEOUT, lim));
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t vd = smem_desc(sbase + Layout::v16 + slot * 2 * kTile, kTile, 1024, 2);
+                        if (elect_one_sync()) {
+#pragma unroll
+                            for (int kk = 0; kk < 8; ++kk)  // 16 tokens each
+                                tc_mma_ts<0>(tmem + kColO + 128u * w, tmem + kColS + 128u * w + 8u * kk,
+                                             vd + ((kk * 16 * 128) >> 4), idesc, b > sg.b0 || kk > 0);
+                            tc_commit(B.pvdone(w));
+                            if (w == nw - 1) tc_commit(B.cempty(slot));
+                        }
+                        __syncwarp();
+                    }
+                }
+            }
+            if (elect_one_sync()) tc_commit(B.drain(1));
+            __syncwarp();
+            mbar_wait_drain(B.drain(1), 0, lim);
+            __syncwarp();
+        } else if (warp >= kConvWarp) {
+            // ==================================================== V: E4M3 bytes -> fp16 operand tiles
+            const int cw = warp - kConvWarp, row8 = lane >> 3, ch = lane & 7;
+            uint32_t it = 0, segs = 0;
+            bool ok = true;
+            while (ok && wk.next(p, sg)) {
+                NanMarks& nm = marks[segs % kMarks];
+                NanMarks& later = marks[(segs + 2) % kMarks];
+                ++segs;
+                for (int b = sg.b0; b < sg.b1 && ok; ++b, ++it) {
+                    const uint32_t vs = it % kNV, cs = it & 1;
+                    ok = warp_ok(mbar_wait_idle(B.vfull(vs), (it / kNV) & 1, abort_flag, p.err, QUP_ERR_TIMEOUT, lim) &&
+                                 mbar_wait_idle(B.cempty(cs), ((it >> 1) & 1) ^ 1, abort_flag, p.err, QUP_ERR_TIMEOUT,
+                                                lim));
+                    if (!ok) break;
+                    // The marks of the segment after the next are cleared.  The other warp comes to them two
+                    // steps later at the earliest, after an O update that waits for this warp's tile here.
+                    // Their last readers, five segments before, are done: the O update two steps ago
+                    // belongs to segment - 2 or later, whose S waited for both warpgroups to have left
+                    // segment - 3.
+                    if (b == sg.b0 && cw == 0) {
+                        for (int d = lane; d < kHeadDim; d += 32) later.first[d] = 0x7fffffff;
+                        if (lane == 0) later.any = 0;
+                        __syncwarp();
+                    }
+                    const uint32_t valid = meta[it % kNM].valid;
+                    const int here = wk.it.q.len - b * kStep;  // tokens of the step that exist
+                    const bool whole = here >= kStep && valid == (1u << PPS) - 1u;
+                    const uint8_t* src = smem + Layout::v + vs * kTile;
+                    uint8_t* dst = smem + Layout::v16 + cs * 2 * kTile;
+#pragma unroll 1
+                    for (int r0 = cw * 64; r0 < cw * 64 + 64; r0 += 32) {
+                    uint4 raw[8];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        const int row = r0 + u * 4 + row8;
+                        raw[u] = *reinterpret_cast<const uint4*>(src + row * 128 + ((ch ^ (row & 7)) << 4));
+                    }
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        const int row = r0 + u * 4 + row8;
+                        uint32_t w4[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+                        if (!whole && (row >= here || !((valid >> (row / T)) & 1u))) w4[0] = w4[1] = w4[2] = w4[3] = 0u;
+                        if (nan_bytes(w4[0]) | nan_bytes(w4[1]) | nan_bytes(w4[2]) | nan_bytes(w4[3])) {
+#pragma unroll 1
+                            for (int x = 0; x < 16; ++x) {
+                                const uint32_t wv = x < 8 ? (x < 4 ? w4[0] : w4[1]) : (x < 12 ? w4[2] : w4[3]);
+                                if (((wv >> (8 * (x & 3))) & 0x7fu) == 0x7fu) atomicMin(&nm.first[16 * ch + x], b * kStep + row);
+                            }
+                            nm.any = 1;
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) w4[x] &= ~((nan_bytes(w4[x]) >> 7) * 0xffu);
+                        }
+                        uint4 o[2];
+                        o[0] = make_uint4(cvt_e4m3x2(w4[0]), cvt_e4m3x2(w4[0] >> 16), cvt_e4m3x2(w4[1]),
+                                          cvt_e4m3x2(w4[1] >> 16));
+                        o[1] = make_uint4(cvt_e4m3x2(w4[2]), cvt_e4m3x2(w4[2] >> 16), cvt_e4m3x2(w4[3]),
+                                          cvt_e4m3x2(w4[3] >> 16));
+                        // 64 columns in each half; lanes of the two halves store their chunks in
+                        // opposite order, so a quarter warp's eight stores meet different banks
+                        const bool hi = ch >= 4;
+                        uint8_t* line = dst + (hi ? kTile : 0) + row * 128;
+                        const int c0 = 2 * (ch & 3) + (hi ? 1 : 0), c1 = c0 ^ 1;
+                        *reinterpret_cast<uint4*>(line + ((c0 ^ (row & 7)) << 4)) = hi ? o[1] : o[0];
+                        *reinterpret_cast<uint4*>(line + ((c1 ^ (row & 7)) << 4)) = hi ? o[0] : o[1];
+                    }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(B.cfull(cs));
+                        mbar_arrive(B.vempty(vs));
+                    }
+                }
+            }
+        }
+    } else {
+        regs_increase<kSoftmaxRegs>();
+        // ======================================================== softmax, epilogue
+        const int w = warp >> 2, wq = warp & 3, r = wq * 32 + lane;
+        const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
+        const uint32_t s_addr = tmem + lane_base + kColS + 128u * w, o_addr = tmem + lane_base + kColO + 128u * w;
+        uint32_t it = 0, use = 0, segs = 0;
+        bool ok = true;
+        while (ok && wk.next(p, sg)) {
+            const NanMarks& nm = marks[segs % kMarks];
+            const bool first_seg = segs == 0;
+            ++segs;
+            const Request& q = wk.it.q;
+            const int row0 = sg.tile * kItemRows + w * kTileRows;  // of the warpgroup, in (query, head) order
+            const int rows = min(kTileRows, wk.it.rows - row0);
+            if (rows <= 0) {  // an empty row tile: the warpgroup reports its place in the walk and waits
+                it += sg.b1 - sg.b0;
+                if (lane == 0) mbar_arrive(B.qfull(w));
+                ok = warp_ok(mbar_wait_idle(B.sdone(), (segs - 1) & 1, abort_flag, p.err, QUP_ERR_TIMEOUT, lim));
+                continue;
+            }
+            const bool on = r < rows;
+            const int x = row0 + (on ? r : rows - 1), qi = x / g, j = x - qi * g;
+            // tokens this row sees, and the warpgroup's first row
+            const int vis = wk.it.ok ? q.len - q.n + qi + 1 : 0;
+            const int vis_all = wk.it.ok ? q.len - q.n + row0 / g + 1 : 0;
+            // ---- Q: high and low E4M3 parts of the row, its score factor
+            float rs;
+            {
+                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.Q) +
+                                                                  (size_t)(q.q0 + qi) * p.q_stride +
+                                                                  (size_t)(sg.h * g + j) * kHeadDim);
+                uint4 raw[16];
+                uint32_t top = 0;
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    raw[c] = __ldg(src + c);
+                    const uint32_t w4[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) top = max(top, max((w4[e] << 16) & 0x7f800000u, w4[e] & 0x7f800000u));
+                }
+                const int ex = max((int)(top >> 23) - 127, -100);  // the largest element is in [2^ex, 2^(ex+1))
+                const float up = __uint_as_float((uint32_t)(7 - ex + 127) << 23);
+                rs = p.scale_log2 * __uint_as_float((uint32_t)(ex - 7 + 127) << 23);
+                if (ex == 128) rs = __uint_as_float(0x7fc00000u);  // an infinity or NaN in the row
+                uint8_t* qt = smem + Layout::q + w * 2 * kTile + r * 128;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint4 v = raw[2 * c + (e >> 1)];
+                        const uint32_t a = (e & 1) ? v.z : v.x, bb = (e & 1) ? v.w : v.y;
+                        const float y[4] = {__uint_as_float(a << 16) * up, __uint_as_float(a & 0xffff0000u) * up,
+                                            __uint_as_float(bb << 16) * up, __uint_as_float(bb & 0xffff0000u) * up};
+                        hi[e] = pack_e4m3x4(y[0], y[1], y[2], y[3]);
+                        const uint32_t h01 = cvt_e4m3x2(hi[e]), h23 = cvt_e4m3x2(hi[e] >> 16);
+                        float z[4];
+                        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+                            : "=f"(z[0]), "=f"(z[1])
+                            : "r"(h01));
+                        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+                            : "=f"(z[2]), "=f"(z[3])
+                            : "r"(h23));
+                        lo[e] = pack_e4m3x4(y[0] - z[0], y[1] - z[1], y[2] - z[2], y[3] - z[3]);
+                    }
+                    const uint32_t at = (uint32_t)((c ^ (r & 7)) << 4);
+                    *reinterpret_cast<uint4*>(qt + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(qt + kTile + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(B.qfull(w));
+            }
+            float m = kNegInf, l = 0.f;
+            for (int b = sg.b0; b < sg.b1; ++b, ++it) {
+                const uint32_t k = use++;
+                ok = warp_ok(mbar_wait(B.mfull(it % kNM), (it / kNM) & 1, abort_flag, p.err, QUP_ERR_TIMEOUT, lim) &&
+                             mbar_wait(B.sfull(w), k & 1, abort_flag, p.err, QUP_ERR_TIMEOUT, lim));
+                if (!ok) break;
+                tc_fence_after();
+                const StepMeta& sm = meta[it % kNM];
+                uint32_t sv[kStep];
+                tmem_ld128_wait(s_addr, sv);
+                const uint32_t valid = sm.valid;
+                const int seen = vis - b * kStep;  // tokens of the step that the row sees
+                float f[PPS], vl[PPS];
+#pragma unroll
+                for (int q2 = 0; q2 < PPS; ++q2) {
+                    const float ks = sm.ks[q2];
+                    vl[q2] = sm.vl[q2];
+                    f[q2] = rs * ks;
+                    if (ks < 0.f) {  // the largest score of the page is that of the smallest product
+#pragma unroll
+                        for (int t = q2 * T; t < (q2 + 1) * T; ++t) sv[t] ^= 0x80000000u;
+                        f[q2] = -f[q2];
+                    }
+                    // a scale of 0 keeps a positive factor: -inf times it stays -inf
+                    if (f[q2] < 1e-30f) f[q2] = 1e-30f;
+                }
+                if (valid != (1u << PPS) - 1u || (b + 1) * kStep > vis_all) {
+#pragma unroll
+                    for (int q2 = 0; q2 < PPS; ++q2) {
+                        const int see = ((valid >> q2) & 1u) ? seen - q2 * T : 0;
+#pragma unroll
+                        for (int t = 0; t < T; ++t)
+                            if (t >= see) sv[q2 * T + t] = __float_as_uint(kNegInf);
+                    }
+                }
+                float bm = kNegInf;
+#pragma unroll
+                for (int q2 = 0; q2 < PPS; ++q2) {
+                    float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+#pragma unroll
+                    for (int t = q2 * T; t < (q2 + 1) * T; t += 8)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            mx[e] = max3f(mx[e], __uint_as_float(sv[t + 2 * e]), __uint_as_float(sv[t + 2 * e + 1]));
+                    bm = fmaxf(bm, fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), f[q2], vl[q2]));
+                }
+                const bool mv = bm > m + kLazy;
+                if (__any_sync(0xffffffffu, mv)) {
+                    const float a = mv ? ex2(m - bm) : 1.f;
+                    if (mv) m = bm;
+                    l *= a;
+                    // S(b) was issued after the last O update had finished: O is free to be rescaled
+                    if (b > sg.b0) {
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t ov[32];
+                            tmem_ld32_wait(o_addr + 32u * c, ov);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * a);
+                            tmem_st_x32(o_addr + 32u * c, ov);
+                        }
+                    }
+                }
+                const float sub = m == kNegInf ? 0.f : m - kOffset;
+#pragma unroll
+                for (int q2 = 0; q2 < PPS; ++q2) {
+                    const f2 ff{f[q2], f[q2]}, off{vl[q2] - sub, vl[q2] - sub};
+                    f2 part[2] = {{0.f, 0.f}, {0.f, 0.f}};
+                    uint32_t ck[8];
+#pragma unroll
+                    for (int t = q2 * T; t < (q2 + 1) * T; t += 2) {
+                        f2 e = fma2(f2{__uint_as_float(sv[t]), __uint_as_float(sv[t + 1])}, ff, off);
+                        e.x = ex2(e.x);
+                        e.y = ex2(e.y);
+                        part[(t >> 1) & 1] = add2(part[(t >> 1) & 1], e);
+                        ck[(t & 15) >> 1] = pack_f16x2(e.x, e.y);
+                        if ((t & 15) == 14) tmem_st_x8(s_addr + (uint32_t)(t >> 1) - 7u, ck);
+                    }
+                    const f2 ps = add2(part[0], part[1]);
+                    const float mass = (ps.x + ps.y) * sm.vi[q2];
+                    l += mass;
+                    if constexpr (WEIGHTS) {
+                        const int pg = b * PPS + q2;
+                        if (on && (long long)pg * T < q.len && wk.it.ok) {
+                            const size_t rowsw = (size_t)p.max_q * g;
+                            p.ws_mass[((size_t)q.p0 * p.c.Hkv + (size_t)sg.h * q.np + pg) * (T / 16) * rowsw + x] =
+                                make_float2(mass, m);
+                        }
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(B.pfull(w));
+            }
+            if (!ok) break;
+            // ---- the row's result, or its part of it
+            ok = warp_ok(mbar_wait(B.pvdone(w), (use - 1) & 1, abort_flag, p.err, QUP_ERR_TIMEOUT, lim));
+            if (!ok) break;
+            tc_fence_after();
+            const bool complete = sg.b0 == 0 && sg.b1 == sg.steps;
+            const size_t part = (size_t)2 * blockIdx.x + (first_seg ? 0 : 1);
+            const size_t prow = part * kItemRows + w * kTileRows + r;
+            const size_t at = (size_t)(q.q0 + qi) * p.Hq + sg.h * g + j;
+            const bool nan = *reinterpret_cast<const volatile int*>(&nm.any) != 0;
+            const float inv = l == 0.f ? 0.f : __fdividef(1.f, l);
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                uint32_t ov[32];
+                tmem_ld32_wait(o_addr + 32u * c, ov);
+                if (nan) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (nm.first[32 * c + e] < vis) ov[e] = 0x7fc00000u;
+                }
+                if (!on) continue;
+                if (complete) {
+                    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.O) + at * kHeadDim + 32 * c);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            o[y] = pack_bf16x2(__uint_as_float(ov[8 * e + 2 * y]) * inv,
+                                               __uint_as_float(ov[8 * e + 2 * y + 1]) * inv);
+                        dst[e] = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                } else {
+                    uint4* dst = reinterpret_cast<uint4*>(p.chunk_o + prow * kHeadDim + 32 * c);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) dst[e] = make_uint4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
+                }
+            }
+            if (on) {
+                if (complete) {
+                    const float l2 = l == 0.f ? kNegInf : m - kOffset + lg2(l);
+                    if (p.lse) p.lse[at] = l2 * 0.69314718055994531f;
+                    if (WEIGHTS) p.ws_lse[at] = l2;
+                } else {
+                    p.chunk_ml[prow] = make_float2(m, l);
+                }
+            }
+            // warpgroup 1 takes part in every phase of this barrier (see the empty row tile)
+            if (w == 1) ok = warp_ok(mbar_wait(B.sdone(), (segs - 1) & 1, abort_flag, p.err, QUP_ERR_TIMEOUT, lim));
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kSWarp) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------ join of cut items
+// CTA (c, y): if the last item of run c begins there and goes on, its rows [32 y, 32 y + 32): the parts
+// of runs c, c + 1, ... in order, up to the run in which the item ends.
+constexpr int kJoinRows = 32;
+__global__ void __launch_bounds__(kHeadDim) cache_chunk_join_kernel(const __grid_constant__ CacheAttnParams p, int runs) {
+    grid_dep_wait();
+    const ChunkSpan a = p.spans[blockIdx.x];
+    if (a.segs == 0 || a.ends || a.b0 != 0) return;
+    const Request q = load_request(p.q_ptr, p.Nq, p.c.kv_len, p.c.page_ptr, p.c.total_pages, p.c.T, a.r);
+    const int rows = min(kItemRows, min(q.n, p.max_q) * p.g - a.tile * kItemRows);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int last = blockIdx.x + 1;
+    while (last < runs - 1 && !p.spans[last].first_ends) ++last;
+    for (int rr = blockIdx.y * kJoinRows + warp; rr < min(rows, (int)(blockIdx.y + 1) * kJoinRows); rr += kHeadDim / 32) {
+        float M = kNegInf, L = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = blockIdx.x; c <= last; ++c) {
+            const size_t part = (size_t)2 * c + (c == (int)blockIdx.x && a.segs > 1 ? 1 : 0);
+            M = fmaxf(M, p.chunk_ml[part * kItemRows + rr].x);
+        }
+        for (int c = blockIdx.x; c <= last; ++c) {
+            const size_t part = (size_t)2 * c + (c == (int)blockIdx.x && a.segs > 1 ? 1 : 0);
+            const size_t at = part * kItemRows + rr;
+            const float2 ml = p.chunk_ml[at];
+            // a part that saw nothing holds zeros; NaN goes through
+            const float f = ml.x == kNegInf ? (ml.y == 0.f ? 0.f : 1.f) : ex2(ml.x - M);
+            const float4 v = reinterpret_cast<const float4*>(p.chunk_o + at * kHeadDim)[lane];
+            L += ml.y * f;
+            acc.x += v.x * f;
+            acc.y += v.y * f;
+            acc.z += v.z * f;
+            acc.w += v.w * f;
+        }
+        const int x = a.tile * kItemRows + rr, qi = x / p.g, j = x - qi * p.g;
+        const size_t at = (size_t)(q.q0 + qi) * p.Hq + a.h * p.g + j;
+        const float inv = L == 0.f ? 0.f : __fdividef(1.f, L);
+        uint2 o;
+        o.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+        o.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+        reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.O) + at * kHeadDim)[lane] = o;
+        if (lane == 0) {
+            const float l2 = L == 0.f ? kNegInf : M - kOffset + lg2(L);
+            if (p.lse) p.lse[at] = l2 * 0.69314718055994531f;
+            if (p.weight) p.ws_lse[at] = l2;
+        }
+    }
+}
+
+template <int T, bool WEIGHTS>
+cudaError_t launch_t(const CUtensorMap& tmK, const CUtensorMap& tmV, const CacheAttnParams& p, int runs,
+                     cudaStream_t stream) {
+    const auto kernel = cache_chunk_kernel<T, WEIGHTS>;
+    // an increase beyond the launch's registers would never be granted: no other count is launched
+    static const int regs = [] {
+        cudaFuncAttributes a;
+        return cudaFuncGetAttributes(&a, (const void*)cache_chunk_kernel<T, WEIGHTS>) == cudaSuccess ? a.numRegs : -1;
+    }();
+    if (regs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+    const size_t smem = cache_chunk_smem();
+    cudaError_t e = ensure_smem_attr((const void*)kernel, smem);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(kernel, dim3(runs), dim3(kThreads), smem, stream, tmK, tmV, p);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(cache_chunk_join_kernel, dim3(runs, kItemRows / kJoinRows), dim3(kHeadDim), 0, stream, p, runs);
+}
+
+template <int T>
+cudaError_t launch_w(const CUtensorMap& tmK, const CUtensorMap& tmV, const CacheAttnParams& p, int runs,
+                     cudaStream_t stream) {
+    return p.weight ? launch_t<T, true>(tmK, tmV, p, runs, stream) : launch_t<T, false>(tmK, tmV, p, runs, stream);
+}
+
+}  // namespace
+
+size_t cache_chunk_smem() { return Layout::total + 1024; }
+
+cudaError_t launch_cache_chunk(const CUtensorMap& tmK, const CUtensorMap& tmV, const CacheAttnParams& p, int runs,
+                               cudaStream_t stream) {
+    switch (p.c.T) {
+        case 16: return launch_w<16>(tmK, tmV, p, runs, stream);
+        case 32: return launch_w<32>(tmK, tmV, p, runs, stream);
+        case 64: return launch_w<64>(tmK, tmV, p, runs, stream);
+        default: return launch_w<128>(tmK, tmV, p, runs, stream);
+    }
+}
+
+}  // namespace qup

@@ -8,6 +8,9 @@ Attention bounds (per element, E = 2^-24 the fp32 half step):
           rescalings, log2 of the V scale) + 2 |ds|, and below fp16's normal range at most 2^-25 where the
           row's largest is at least 2^8: 2^-33 of the largest |v| for each token
   O       those against sum p|v|, and bf16's half step 2^-8 of |O|
+  scores of requests with more than 16 rows: Q's low part is within 2^-17 of the row's largest element
+          where that is coarser than its last bit, so |ds| grows by 2^-17 max|q| sum|k|, which is at most
+          2^-17 * (sum|q||k| max|q| sum|k| / sum|q||k|); the oracle returns qk = max|q| sum|k| (scaled)
   lse     |ds| + 2^-18 + E |lse| + E * tokens (the sum of weights, in order)
   page weights  a relative 2 |ds| + 2^-17 + 2 E * tokens
 """
@@ -84,7 +87,7 @@ def _ptr(ns):
 
 
 def _check_attn(got, lse, weight, ref, tokens, what, p_round=2.0 ** -11):
-    ds = 2.0 ** -16 * ref["smag"]
+    ds = 2.0 ** -16 * ref["smag"] + 2.0 ** -17 * ref["qk"]
     rel = p_round + 2.0 ** -18 + 2 * ds
     tol = 2.0 ** -8 * np.abs(ref["o"]) + rel[..., None] * ref["vmag"] + (tokens * 2.0 ** -33 * ref["vtop"])[..., None]
     err = np.abs(got - ref["o"])
@@ -227,7 +230,8 @@ def test_short_runs_match_the_oracle(T, g, n):
     _check_attn(o, lse, w, ref, 500, (T, g, n))
 
 
-@pytest.mark.parametrize("T,g,n,L", [(64, 4, 100, 400), (16, 3, 77, 77), (32, 8, 65, 1000), (128, 1, 200, 260)])
+@pytest.mark.parametrize("T,g,n,L", [(64, 4, 100, 400), (16, 3, 77, 77), (32, 8, 65, 1000), (128, 1, 200, 260),
+                                     (64, 40, 30, 190), (16, 8, 33, 900)])
 def test_chunks_match_the_oracle(T, g, n, L):
     c = Case(T + n, [L, L - 3, n // 2], T=T)
     o, lse, w, ref = _run_attn(c, [n, n - 5, n // 2], g, weights=False)
@@ -304,9 +308,71 @@ def test_nan_tokens_reach_only_the_rows_that_see_them():
     assert np.array_equal(nan_o, want) and want.any()
     assert np.array_equal(np.isnan(lse), np.isnan(ref["lse"]))
     ok = ~want.any(axis=2)
-    for k in ("o", "lse", "smag", "vmag", "vtop"):
+    for k in ("o", "lse", "smag", "vmag", "vtop", "qk"):
         ref[k] = ref[k][ok]
     _check_attn(o[ok], lse[ok], None, ref, 100, "beside NaN")
+
+
+def test_nan_tokens_of_a_chunk_reach_only_the_rows_that_see_them():
+    c = Case(18, [300, 200, 260], T=32)
+    c.V[c.table[c.page_ptr[0] + 7], 0, 5, 9] = 0x7F   # request 0, token 229
+    c.V[c.table[c.page_ptr[0] + 8], 0, 0, 70] = 0xFF  # and 256, another column
+    c.K[c.table[c.page_ptr[1] + 5], 1, 2, 0] = 0xFF   # request 1, token 162
+    o, lse, w, ref = _run_attn(c, [90, 60, 40], 4, weights=False)
+    want = np.isnan(ref["o"])
+    assert np.array_equal(np.isnan(o), want) and want.any()
+    assert np.array_equal(np.isnan(lse), np.isnan(ref["lse"]))
+    ok = ~want.any(axis=2)
+    for k in ("o", "lse", "smag", "vmag", "vtop", "qk"):
+        ref[k] = ref[k][ok]
+    _check_attn(o[ok], lse[ok], None, ref, 300, "beside NaN")
+
+
+def test_small_and_large_requests_in_one_batch():
+    c = Case(19, [500, 90, 700, 0, 33, 1200, 256], T=64)
+    ns = [1, 90, 40, 0, 3, 1, 256]
+    o, lse, w, ref = _run_attn(c, ns, 4)
+    _check_attn(o, lse, w, ref, 1200, "mixed rows")
+
+
+def test_many_requests_of_a_few_rows_share_the_grid():
+    rng = np.random.default_rng(21)
+    lens = [int(x) for x in rng.integers(5, 260, 170)] + [2000]
+    c = Case(21, lens, T=32)
+    o, lse, w, ref = _run_attn(c, [5] * len(lens), 5)
+    _check_attn(o, lse, w, ref, 2000, "few rows")
+    # and a few of more than one row tile between them
+    ns = [40 if r % 9 == 4 and lens[r] > 40 else 4 for r in range(len(lens))]
+    o, lse, w, ref = _run_attn(c, ns, 5)
+    _check_attn(o, lse, w, ref, 2000, "few and more rows")
+
+
+def test_bad_pages_scales_and_lengths_in_chunks():
+    torch = _t()
+    c = Case(20, [300, 300, 300, 300], T=64)
+    p = [c.table[c.page_ptr[r]:c.page_ptr[r + 1]] for r in range(4)]
+    bad = [int(c.page_ptr[0]) + 1, int(p[1][2]), int(c.page_ptr[3])]
+    ns = [40, 40, 40, 40]
+    ptr = _ptr(ns)
+    qv, qt = _bf16(c.rng.standard_normal((160, 8, 128)))
+    good = oc.attn(qv, c.K, c.V, c.ks, c.vs, c.table, c.page_ptr, c.lens, ptr, 1 / math.sqrt(128))
+    c.table[bad[0]] = -7
+    c.vs[bad[1]] = np.nan
+    c.lens[3] = 10 ** 7
+    o = qup.cache_attn(c.cache(), qt, torch.from_numpy(ptr).cuda(), 40)
+    assert qup.get_error() == qup.ERR["PHYS_PAGE"] | qup.ERR["SCALE"] | qup.ERR["GROUP"]
+    assert torch.isfinite(o).all() and torch.all(o[120:] == 0)
+    ref = {k: v[80:120] for k, v in good.items() if k != "weight"}
+    _check_attn(o[80:120].double().cpu().numpy(), None, None, ref, 300, "the good request")
+    # the pages that are not seen: the oracle over the others
+    c.lens[3] = 300
+    sel = np.array([[0, 2, 3, 4], [0, 1, 3, 4], [0, 1, 2, 3], [-1, -1, -1, -1]])
+    topk = np.broadcast_to(np.repeat(sel, 40, axis=0), (8, 160, 4)).astype(np.int32)
+    c.table[bad[0]] = 0
+    c.vs[bad[1]] = 1
+    part = oc.attn(qv, c.K, c.V, c.ks, c.vs, c.table, c.page_ptr, c.lens, ptr, 1 / math.sqrt(128), topk)
+    ref = {k: v[:80] for k, v in part.items() if k != "weight"}
+    _check_attn(o[:80].double().cpu().numpy(), None, None, ref, 300, "pages not seen")
 
 
 def test_query_with_infinite_elements_gives_nan_and_leaves_others():
@@ -318,7 +384,7 @@ def test_query_with_infinite_elements_gives_nan_and_leaves_others():
     bad = np.zeros((2, 8), bool)
     bad[0, 3] = bad[1, 1] = True
     assert np.isnan(o[bad]).all()
-    for k in ("o", "lse", "smag", "vmag", "vtop"):
+    for k in ("o", "lse", "smag", "vmag", "vtop", "qk"):
         ref[k] = ref[k][~bad]
     _check_attn(o[~bad], lse[~bad], None, ref, 90, "beside inf")
 
