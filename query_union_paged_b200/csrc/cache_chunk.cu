@@ -18,10 +18,9 @@
 // visible steps are laid end to end and cut into one equal run per CTA (one per SM); an item cut by a
 // run's end leaves partial results, which a second kernel joins in a fixed order.
 //
-// Warps (384 threads): 0-3 and 4-7 softmax of row tile 0 and 1 (thread = row); 8 loads the K and V bytes
-// by TMA two steps ahead and issues S; 9 issues O += P V; 10 and 11 convert V tiles to fp16 in the
-// 128-byte-swizzled MN-major operand layout.  P goes over S in TMEM.  The loads share a warp with S at
-// no loss: what a load waits for (S of an earlier step, a converted V tile) the next S waits for too.
+// Warps (384 threads): 0-3 and 4-7 softmax of row tile 0 and 1 (thread = row); 8 issues S and O += P V,
+// 9 loads K and V bytes by TMA and the pages' constants; 10 and 11 convert V tiles to fp16 in the
+// 128-byte-swizzled MN-major operand layout.  P goes over S in TMEM.
 //
 // NaN: a NaN byte of V that a row does not see must not reach it as 0 * NaN.  The converters store 0 for
 // it and remember its column's first such token; the epilogue gives NaN to the rows that see it.
@@ -41,27 +40,26 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kStep = 128;                  // tokens of a step
+constexpr int kCols = 32;                   // scores that a softmax thread works on at a time
 constexpr int kTileRows = 128;              // rows of a warpgroup
 constexpr int kItemRows = kChunkRows;       // rows of an item
 constexpr int kTile = kStep * kHeadDim;     // bytes of a K or V tile
 constexpr int kNK = 3, kNV = 2, kNM = 8;    // K tiles, V tiles, page constants in flight
+constexpr int kConvRows = 2;                // rows of V that a converting lane has in hand
 constexpr int kMarks = 5;                   // segments whose NaN marks are held
 constexpr int kMaxPages = kStep / 16;
-constexpr int kSWarp = 8, kPvWarp = 9, kConvWarp = 10, kConvWarps = 2;
-constexpr int kAhead = 2;                   // steps that the loads are ahead of S
-// registers: the launch gives 384 x 168; the softmax warpgroups take 208 each, the others keep 88
-constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
-static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "register split");
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kConvWarp = 10, kConvWarps = 2;
 constexpr uint32_t kColO = 0, kColS = 256;
+constexpr int kPolyPairs = 3;      // of every eight pairs of exponentials, those on the FMA pipe
 constexpr float kOffset = 8.f;     // log2 offset of P
 constexpr float kLazy = 7.f;       // the maximum moves once a score passes it by this: P <= 2^15
 constexpr float kZeroScaleLog2 = -64.f;
 constexpr float kNegInf = -INFINITY;
 
-struct StepMeta {  // the pages of a step
-    float ks[kMaxPages], vl[kMaxPages], vi[kMaxPages];
-    uint32_t valid;
-    uint32_t pad[7];
+struct __align__(16) StepMeta {  // the pages of a step
+    float4 page[kMaxPages];  // ks, log2 vs, 1 / vs
+    uint32_t valid, negative;  // pages that are seen, that have a negative K scale
+    uint32_t pad[2];
 };
 
 struct NanMarks {  // of one segment
@@ -70,6 +68,7 @@ struct NanMarks {  // of one segment
     int pad[3];
 };
 
+struct WarpWalk;
 struct Layout {
     static constexpr uint32_t q = 0;                                // [2][hi, lo][128][128]
     static constexpr uint32_t k = q + 4 * kTile;                    // [kNK]
@@ -80,7 +79,8 @@ struct Layout {
     static constexpr uint32_t bars = nan + kMarks * sizeof(NanMarks);
     static constexpr uint32_t scan = bars + 8 * 40;                 // [kThreads] int64
     static constexpr uint32_t misc = scan + 8 * kThreads;
-    static constexpr uint32_t total = misc + 64;
+    static constexpr uint32_t walks = misc + 64;                    // one per warp
+    static constexpr uint32_t total = walks + (kThreads / 32) * 128;
 };
 
 __device__ __forceinline__ float lg2(float x) {
@@ -98,22 +98,32 @@ __device__ __forceinline__ uint32_t cvt_e4m3x2(uint32_t v) {  // low 16 bits
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)v));
     return r;
 }
+__device__ __forceinline__ void f16x2_to_f32(uint32_t v, float& lo, float& hi) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+        : "=f"(lo), "=f"(hi)
+        : "r"(v));
+}
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {  // NaN if any is
+    float y;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {  // 0x80 at each E4M3 NaN (0x7f, 0xff)
     return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
 }
 
-// sum over t in [0, n) of floor((a t + b) / m), all non-negative
-__device__ long long floor_sum(long long n, long long m, long long a, long long b) {
+// sum over t in [0, n) of floor((a t + b) / m); a n + b fits 32 bits
+__device__ long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
     long long s = 0;
     while (n > 0) {
-        s += (n - 1) * n / 2 * (a / m) + n * (b / m);
+        s += (long long)((unsigned long long)(n - 1) * n / 2) * (a / m) + (long long)n * (b / m);
         a %= m;
         b %= m;
-        const long long y = a * n + b;
+        const uint32_t y = a * n + b;
         if (y < m) break;
         n = y / m;
         b = y % m;
-        const long long x = m;
+        const uint32_t x = m;
         m = a;
         a = x;
     }
@@ -141,12 +151,12 @@ struct Items {
     __device__ __forceinline__ int steps(const CacheAttnParams& p, int t) const {
         if (!ok) return 1;
         const int last = min((t + 1) * kItemRows, rows) - 1;
-        return (int)(((long long)p.g * (base + kStep - 1) + last) / ((long long)kStep * p.g));
+        return (int)((uint32_t)(p.g * (base + kStep - 1) + last) / (uint32_t)(kStep * p.g));
     }
     // steps of the first t < nt row tiles
     __device__ __forceinline__ long long before(const CacheAttnParams& p, int t) const {
         if (!ok) return t;
-        return floor_sum(t, (long long)kStep * p.g, kItemRows, (long long)p.g * (base + kStep - 1) + kItemRows - 1);
+        return floor_sum(t, kStep * p.g, kItemRows, p.g * (base + kStep - 1) + kItemRows - 1);
     }
     __device__ __forceinline__ long long total(const CacheAttnParams& p) const {
         return nt == 0 ? 0 : (before(p, nt - 1) + steps(p, nt - 1)) * p.c.Hkv;
@@ -203,6 +213,26 @@ struct Walk {  // a CTA's run of steps, item by item
     }
 };
 
+// A warp's walk and the segment it is in, in shared memory (kept in registers, they would be spilled
+// around the softmax loop, to local memory for which little L1 is left): lane 0 moves it on.
+struct WarpWalk {
+    Walk wk;
+    Seg sg;
+    int more;
+    __device__ __forceinline__ void begin(const int* start, int lane) {
+        if (lane == 0) wk.begin(start);
+        __syncwarp();
+    }
+    __device__ __forceinline__ bool next(const CacheAttnParams& p, int lane) {
+        __syncwarp();
+        if (lane == 0) more = wk.next(p, sg);
+        __syncwarp();
+        return more != 0;
+    }
+};
+
+static_assert(sizeof(WarpWalk) <= 128, "a warp's walk");
+
 struct Bars {
     uint32_t base;
     __device__ __forceinline__ uint32_t at(int i) const { return base + 8u * i; }
@@ -214,14 +244,14 @@ struct Bars {
     __device__ __forceinline__ uint32_t cfull(int s) const { return f(s); }       // fp16 V written
     __device__ __forceinline__ uint32_t cempty(int s) const { return f(2 + s); }  // fp16 V read
     __device__ __forceinline__ uint32_t sfull(int w) const { return f(4 + w); }
-    __device__ __forceinline__ uint32_t pfull(int w) const { return f(6 + w); }
+    __device__ __forceinline__ uint32_t pfull(int w, int half) const { return f(15 + 2 * w + half); }
     __device__ __forceinline__ uint32_t pvdone(int w) const { return f(8 + w); }
     __device__ __forceinline__ uint32_t qfull(int w) const { return f(10 + w); }
-    __device__ __forceinline__ uint32_t drain(int i) const { return f(12 + i); }
-    __device__ __forceinline__ uint32_t sdone() const { return f(14); }  // every S of a segment issued
-    __device__ __forceinline__ uint32_t mfull(int s) const { return f(15 + s); }
+    __device__ __forceinline__ uint32_t drain() const { return f(12); }
+    __device__ __forceinline__ uint32_t sdone() const { return f(14); }  // a segment's products are done
+    __device__ __forceinline__ uint32_t mfull(int s) const { return f(19 + s); }
 };
-static_assert(2 * kNK + 2 * kNV + 15 + kNM <= 40, "barrier block");
+static_assert(2 * kNK + 2 * kNV + 19 + kNM <= 40, "barrier block");
 
 __device__ __forceinline__ bool warp_ok(bool ok) { return __all_sync(0xffffffffu, ok); }
 
@@ -229,7 +259,7 @@ template <int T, bool WEIGHTS>
 __global__ void __launch_bounds__(kThreads, 1)
     cache_chunk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                        const __grid_constant__ CacheAttnParams p) {
-    constexpr int PPS = kStep / T;
+    constexpr int PPS = kStep / T, TC = T < kCols ? T : kCols;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
@@ -257,11 +287,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(B.cfull(s), kConvWarps);
             mbar_init(B.cempty(s), 1);
             mbar_init(B.sfull(s), 1);
-            mbar_init(B.pfull(s), 4);
+            mbar_init(B.pfull(s, 0), 4);
+            mbar_init(B.pfull(s, 1), 4);
             mbar_init(B.pvdone(s), 1);
             mbar_init(B.qfull(s), 4);
-            mbar_init(B.drain(s), 1);
         }
+        mbar_init(B.drain(), 1);
         mbar_init(B.sdone(), 1);
         for (int s = 0; s < kNM; ++s) mbar_init(B.mfull(s), 1);
         *abort_flag = 0;
@@ -271,11 +302,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = tid; i < kMarks * (int)(sizeof(NanMarks) / 4); i += kThreads)
         reinterpret_cast<int*>(marks)[i] = i % (int)(sizeof(NanMarks) / 4) < kHeadDim ? 0x7fffffff : 0;
-    if (tid == kSWarp * 32) {
+    if (tid == kLoadWarp * 32) {
         prefetch_tensormap(&tmK);
         prefetch_tensormap(&tmV);
     }
-    if (warp == kSWarp) {
+    if (warp == kMmaWarp) {
         tmem_alloc(smem_u32((const void*)tmem_slot), 512);
         tmem_relinquish();
     }
@@ -334,52 +365,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncthreads();
     }
 
-    Walk wk;
-    wk.begin(s_start);
-    Seg sg;
+    WarpWalk& ww = *reinterpret_cast<WarpWalk*>(smem + Layout::walks + warp * 128);
+    const Walk& wk = ww.wk;
+    const Seg& sg = ww.sg;
+    ww.begin(s_start, lane);
 
     if (warp >= 8) {
-        regs_decrease<kOtherRegs>();
-        if (warp == kSWarp) {
-            // ==================================================== loads and S
-            Walk lead;  // of the loads
-            lead.begin(s_start);
-            Seg ls{};
+        if (warp == kLoadWarp) {
+            // ==================================================== it
             ChunkSpan info{};
-            int lb = 0;         // the next step to load
-            bool more = true;
-            uint32_t loads = 0;
-            int have0 = 0, have1 = 0, phys = -1;  // page table entries that the lanes hold
-            float ks = 0.f, vl = 0.f, vi = 0.f;
-            const auto load_next = [&]() -> bool {  // false: a wait gave up
-                if (!more) return true;
-                if (lb >= ls.b1) {
-                    more = lead.next(p, ls);
-                    if (!more) return true;
-                    info.r = ls.r;
-                    info.h = ls.h;
-                    info.tile = ls.tile;
-                    info.b0 = ls.b0;
-                    info.ends = ls.b1 == ls.steps;
-                    if (info.segs == 0) info.first_ends = info.ends;
-                    ++info.segs;
-                    lb = ls.b0;
-                    have1 = 0;
-                }
-                const int pe = lb * PPS;
+            uint32_t it = 0;
+            bool ok = true;
+            while (ok && ww.next(p, lane)) {
+                info.r = sg.r;
+                info.h = sg.h;
+                info.tile = sg.tile;
+                info.b0 = sg.b0;
+                info.ends = sg.b1 == sg.steps;
+                if (info.segs == 0) info.first_ends = info.ends;
+                ++info.segs;
+                const int b1 = sg.b1, h = sg.h, last = wk.it.ok ? (wk.it.q.len + T - 1) / T : 0, p0 = wk.it.q.p0;
+                int have0 = 0, have1 = 0, phys = -1;  // page table entries that the lanes hold
+                float ks = 0.f, vl = 0.f, vi = 0.f;
+                for (int b = sg.b0; b < b1 && ok; ++b, ++it) {
+                    const int pe = b * PPS;
                 if (pe + PPS > have1) {
                     have0 = pe;
                     have1 = pe + 32;
-                    const int e = pe + lane, last = lead.it.ok ? (lead.it.q.len + T - 1) / T : 0;
+                    const int e = pe + lane;
                     phys = -1;
                     if (e < last) {
-                        phys = p.c.page_table[lead.it.q.p0 + e];
+                        phys = p.c.page_table[p0 + e];
                         if (phys < 0 || phys >= p.c.P_phys) {
                             atomicOr(p.err, QUP_ERR_PHYS_PAGE);
                             phys = -1;
                         } else {
-                            ks = __ldg(p.c.k_scale + (size_t)phys * p.c.Hkv + ls.h);
-                            const float vs = __ldg(p.c.v_scale + (size_t)phys * p.c.Hkv + ls.h);
+                            ks = __ldg(p.c.k_scale + (size_t)phys * p.c.Hkv + h);
+                            const float vs = __ldg(p.c.v_scale + (size_t)phys * p.c.Hkv + h);
                             if (!(fabsf(ks) < INFINITY) || !(vs >= 0.f && vs < INFINITY)) {
                                 atomicOr(p.err, QUP_ERR_SCALE);
                                 phys = -1;
@@ -392,25 +414,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const int src = pe - have0;
                 const uint32_t live = (__ballot_sync(0xffffffffu, phys >= 0) >> src) & ((1u << PPS) - 1u);
+                const uint32_t neg = (__ballot_sync(0xffffffffu, ks < 0.f) >> src) & ((1u << PPS) - 1u);
                 const uint32_t bytes = __popc(live) * T * kHeadDim;
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
                     const int n = kv ? kNV : kNK;
-                    const uint32_t slot = loads % n, par = (loads / n) & 1;
+                    const uint32_t slot = it % n, par = (it / n) & 1;
                     if (!warp_ok(mbar_wait_idle(kv ? B.vempty(slot) : B.kempty(slot), par ^ 1, abort_flag, p.err,
                                                 QUP_ERR_TIMEOUT, lim)))
-                        return false;
+                        ok = false;
+                    if (!ok) break;
                     if (kv == 0) {
                         // the constants' last readers, kNM steps ago, are done: S of a later step has run
-                        StepMeta& m = meta[loads % kNM];
-                        if (lane >= src && lane < src + PPS) {
-                            m.ks[lane - src] = ks;
-                            m.vl[lane - src] = vl;
-                            m.vi[lane - src] = vi;
+                        StepMeta& m = meta[it % kNM];
+                        if (lane >= src && lane < src + PPS) m.page[lane - src] = make_float4(ks, vl, vi, 0.f);
+                        if (lane == 0) {
+                            m.valid = live;
+                            m.negative = neg;
                         }
-                        if (lane == 0) m.valid = live;
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(B.mfull(loads % kNM));
+                        if (lane == 0) mbar_arrive(B.mfull(it % kNM));
                     }
                     const uint32_t full = kv ? B.vfull(slot) : B.kfull(slot);
                     if (lane == 0) {
@@ -421,105 +444,103 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane >= src && lane < src + PPS && phys >= 0)
                         tma_load_4d(sbase + (kv ? Layout::v : Layout::k) + slot * kTile +
                                         (uint32_t)(lane - src) * T * kHeadDim,
-                                    kv ? &tmV : &tmK, full, 0, 0, ls.h, phys);
+                                    kv ? &tmV : &tmK, full, 0, 0, h, phys);
                     __syncwarp();
                 }
-                ++loads;
-                ++lb;
-                return true;
-            };
-            constexpr uint32_t idesc = instr_desc(0, 0, 0, kStep, kTileRows);
-            uint32_t it = 0, use[2] = {0, 0}, segs = 0;
-            bool ok = true;
-            for (int a = 0; a < kAhead && ok; ++a) ok = load_next();
-            while (ok && wk.next(p, sg)) {
-                const int nw = min(kItemRows, wk.it.rows - sg.tile * kItemRows) > kTileRows ? 2 : 1;
-                const uint32_t sp = segs++ & 1;
-                if (nw == 1) ok = warp_ok(mbar_wait_idle(B.qfull(1), sp, abort_flag, p.err, QUP_ERR_TIMEOUT, lim));
-                for (int b = sg.b0; b < sg.b1 && ok; ++b, ++it) {
-                    const uint32_t slot = it % kNK;
-                    ok = warp_ok(mbar_wait_idle(B.kfull(slot), (it / kNK) & 1, abort_flag, p.err, QUP_ERR_TIMEOUT, lim));
-                    for (int w = 0; w < nw && ok; ++w) {
-                        const uint32_t k = use[w]++;
-                        // S_w is free once the O update that last read P from it is done
-                        ok = warp_ok((b > sg.b0 ||
-                                      mbar_wait_idle(B.qfull(w), sp, abort_flag, p.err, QUP_ERR_TIMEOUT, lim)) &&
-                                     (k == 0 || mbar_wait_idle(B.pvdone(w), (k - 1) & 1, abort_flag, p.err,
-                                                               QUP_ERR_TIMEOUT, lim)));
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint64_t qd = smem_desc(sbase + Layout::q + w * 2 * kTile, 16, 1024, 2);
-                        const uint64_t kd = smem_desc(sbase + Layout::k + slot * kTile, 16, 1024, 2);
-                        if (elect_one_sync()) {
-#pragma unroll
-                            for (int kk = 0; kk < 8; ++kk)  // the low parts of Q first
-                                tc_mma<2>(tmem + kColS + 128u * w, qd + (((kk < 4 ? kTile : 0) + (kk & 3) * 32) >> 4),
-                                          kd + (((kk & 3) * 32) >> 4), idesc, kk > 0);
-                            tc_commit(B.sfull(w));
-                            if (w == nw - 1) tc_commit(B.kempty(slot));
-                        }
-                        __syncwarp();
-                    }
-                    if (ok) ok = load_next();
                 }
-                if (lane == 0) mbar_arrive(B.sdone());
-                __syncwarp();
             }
-            if (elect_one_sync()) tc_commit(B.drain(0));
-            __syncwarp();
-            mbar_wait_drain(B.drain(0), 0, lim);
             if (lane == 0) {
                 p.spans[blockIdx.x] = info;
                 if (*abort_flag) {  // what is in flight lands before the CTA leaves
-                    for (uint32_t k = loads > (uint32_t)kNK ? loads - kNK : 0; k <= loads; ++k)
+                    for (uint32_t k = it > (uint32_t)kNK ? it - kNK : 0; k <= it; ++k)
                         mbar_wait_drain(B.kfull(k % kNK), (k / kNK) & 1, lim / 16);
-                    for (uint32_t k = loads > (uint32_t)kNV ? loads - kNV : 0; k <= loads; ++k)
+                    for (uint32_t k = it > (uint32_t)kNV ? it - kNV : 0; k <= it; ++k)
                         mbar_wait_drain(B.vfull(k % kNV), (k / kNV) & 1, lim / 16);
                 }
             }
             __syncwarp();
-        } else if (warp == kPvWarp) {
-            // ==================================================== O += P V
-            constexpr uint32_t idesc = instr_desc(0, 0, 1, kHeadDim, kTileRows);
-            uint32_t it = 0, use[2] = {0, 0};
+        } else if (warp == kMmaWarp) {
+            // ==================================================== S = Q K^T and O += P V
+            constexpr uint32_t idesc_s = instr_desc(0, 0, 0, kStep, kTileRows);
+            constexpr uint32_t idesc_o = instr_desc(0, 0, 1, kHeadDim, kTileRows);
+            uint32_t it = 0, use[2] = {0, 0}, segs = 0;
             bool ok = true;
-            while (ok && wk.next(p, sg)) {
+            const auto wait = [&](uint32_t bar, uint32_t parity) {
+                ok = ok && warp_ok(mbar_wait_idle(bar, parity & 1, abort_flag, p.err, QUP_ERR_TIMEOUT, lim));
+                if (ok) tc_fence_after();
+                return ok;
+            };
+            const auto issue_s = [&](int w, uint32_t slot, bool last) {
+                const uint64_t qd = smem_desc(sbase + Layout::q + w * 2 * kTile, 16, 1024, 2);
+                const uint64_t kd = smem_desc(sbase + Layout::k + slot * kTile, 16, 1024, 2);
+                if (elect_one_sync()) {
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)  // the low parts of Q first
+                        tc_mma<2>(tmem + kColS + 128u * w, qd + (((kk < 4 ? kTile : 0) + (kk & 3) * 32) >> 4),
+                                  kd + (((kk & 3) * 32) >> 4), idesc_s, kk > 0);
+                    tc_commit(B.sfull(w));
+                    if (last) tc_commit(B.kempty(slot));
+                }
+                __syncwarp();
+            };
+            while (ok && ww.next(p, lane)) {
                 const int nw = min(kItemRows, wk.it.rows - sg.tile * kItemRows) > kTileRows ? 2 : 1;
-                for (int b = sg.b0; b < sg.b1 && ok; ++b, ++it) {
-                    const uint32_t slot = it & 1;
-                    ok = warp_ok(mbar_wait_idle(B.cfull(slot), (it >> 1) & 1, abort_flag, p.err, QUP_ERR_TIMEOUT, lim));
+                const uint32_t sp = segs++ & 1;
+                const int b0 = sg.b0, b1 = sg.b1;
+                // the first S: both warpgroups have come to the segment (one may have no rows in it), and
+                // the O updates that last read P from the S buffers are done (at the end of a segment
+                // they are waited for below)
+                wait(B.qfull(0), sp);
+                wait(B.qfull(1), sp);
+                if (!wait(B.kfull(it % kNK), it / kNK)) break;
+                for (int w = 0; w < nw; ++w) issue_s(w, it % kNK, w == nw - 1);
+                for (int b = b0; b < b1 && ok; ++b, ++it) {
+                    if (!wait(B.cfull(it & 1), it >> 1)) break;
                     for (int w = 0; w < nw && ok; ++w) {
                         const uint32_t k = use[w]++;
-                        ok = warp_ok(mbar_wait_idle(B.pfull(w), k & 1, abort_flag, p.err, QUP_ERR_TIMEOUT, lim));
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint64_t vd = smem_desc(sbase + Layout::v16 + slot * 2 * kTile, kTile, 1024, 2);
-                        if (elect_one_sync()) {
+                        const uint64_t vd = smem_desc(sbase + Layout::v16 + (it & 1) * 2 * kTile, kTile, 1024, 2);
+                        for (int half = 0; half < 2; ++half) {  // tokens 0 .. 63, then 64 .. 127
+                            if (!wait(B.pfull(w, half), k)) break;
+                            if (elect_one_sync()) {
 #pragma unroll
-                            for (int kk = 0; kk < 8; ++kk)  // 16 tokens each
-                                tc_mma_ts<0>(tmem + kColO + 128u * w, tmem + kColS + 128u * w + 8u * kk,
-                                             vd + ((kk * 16 * 128) >> 4), idesc, b > sg.b0 || kk > 0);
-                            tc_commit(B.pvdone(w));
-                            if (w == nw - 1) tc_commit(B.cempty(slot));
+                                for (int kk = 0; kk < 4; ++kk)  // 16 tokens each
+                                    tc_mma_ts<0>(tmem + kColO + 128u * w, tmem + kColS + 128u * w + 32u * half + 8u * kk,
+                                                 vd + (((4 * half + kk) * 16 * 128) >> 4), idesc_o,
+                                                 b > b0 || half > 0 || kk > 0);
+                                if (half == 1) tc_commit(B.pvdone(w));
+                                if (half == 1 && w == nw - 1) tc_commit(B.cempty(it & 1));
+                            }
+                            __syncwarp();
                         }
-                        __syncwarp();
+                        // the tile's next S, over the P that this update read
+                        if (b + 1 < b1) {
+                            if (w == 0) wait(B.kfull((it + 1) % kNK), (it + 1) / kNK);
+                            if (!wait(B.pvdone(w), k)) break;
+                            issue_s(w, (it + 1) % kNK, w == nw - 1);
+                        } else {
+                            wait(B.pvdone(w), k);
+                        }
                     }
                 }
+                if (lane == 0) mbar_arrive(B.sdone());
+                __syncwarp();
             }
-            if (elect_one_sync()) tc_commit(B.drain(1));
+            if (elect_one_sync()) tc_commit(B.drain());
             __syncwarp();
-            mbar_wait_drain(B.drain(1), 0, lim);
+            mbar_wait_drain(B.drain(), 0, lim);
             __syncwarp();
         } else if (warp >= kConvWarp) {
             // ==================================================== V: E4M3 bytes -> fp16 operand tiles
             const int cw = warp - kConvWarp, row8 = lane >> 3, ch = lane & 7;
             uint32_t it = 0, segs = 0;
             bool ok = true;
-            while (ok && wk.next(p, sg)) {
+            while (ok && ww.next(p, lane)) {
                 NanMarks& nm = marks[segs % kMarks];
                 NanMarks& later = marks[(segs + 2) % kMarks];
+                const int len = wk.it.q.len;
                 ++segs;
-                for (int b = sg.b0; b < sg.b1 && ok; ++b, ++it) {
+                const int b0 = sg.b0, b1 = sg.b1;
+                for (int b = b0; b < b1 && ok; ++b, ++it) {
                     const uint32_t vs = it % kNV, cs = it & 1;
                     ok = warp_ok(mbar_wait_idle(B.vfull(vs), (it / kNV) & 1, abort_flag, p.err, QUP_ERR_TIMEOUT, lim) &&
                                  mbar_wait_idle(B.cempty(cs), ((it >> 1) & 1) ^ 1, abort_flag, p.err, QUP_ERR_TIMEOUT,
@@ -530,52 +551,62 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // Their last readers, five segments before, are done: the O update two steps ago
                     // belongs to segment - 2 or later, whose S waited for both warpgroups to have left
                     // segment - 3.
-                    if (b == sg.b0 && cw == 0) {
+                    if (b == b0 && cw == 0) {
                         for (int d = lane; d < kHeadDim; d += 32) later.first[d] = 0x7fffffff;
                         if (lane == 0) later.any = 0;
                         __syncwarp();
                     }
                     const uint32_t valid = meta[it % kNM].valid;
-                    const int here = wk.it.q.len - b * kStep;  // tokens of the step that exist
+                    const int here = len - b * kStep;  // tokens of the step that exist
+                    const uint8_t* src = smem + Layout::v + vs * kTile + row8 * 128;
+                    uint8_t* dst = smem + Layout::v16 + cs * 2 * kTile + row8 * 128;
                     const bool whole = here >= kStep && valid == (1u << PPS) - 1u;
-                    const uint8_t* src = smem + Layout::v + vs * kTile;
-                    uint8_t* dst = smem + Layout::v16 + cs * 2 * kTile;
+                    // a quarter of a warp's lanes share a row of 128 bytes: 16 each (rolled, as the softmax
+                    // loops are)
 #pragma unroll 1
-                    for (int r0 = cw * 64; r0 < cw * 64 + 64; r0 += 32) {
-                    uint4 raw[8];
+                    for (int r0 = cw * (kStep / kConvWarps); r0 < (cw + 1) * (kStep / kConvWarps); r0 += 4 * kConvRows) {
+                        uint4 raw[kConvRows];
+                        uint32_t odd = 0;  // a NaN among them
 #pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        const int row = r0 + u * 4 + row8;
-                        raw[u] = *reinterpret_cast<const uint4*>(src + row * 128 + ((ch ^ (row & 7)) << 4));
-                    }
-#pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        const int row = r0 + u * 4 + row8;
-                        uint32_t w4[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
-                        if (!whole && (row >= here || !((valid >> (row / T)) & 1u))) w4[0] = w4[1] = w4[2] = w4[3] = 0u;
-                        if (nan_bytes(w4[0]) | nan_bytes(w4[1]) | nan_bytes(w4[2]) | nan_bytes(w4[3])) {
-#pragma unroll 1
-                            for (int x = 0; x < 16; ++x) {
-                                const uint32_t wv = x < 8 ? (x < 4 ? w4[0] : w4[1]) : (x < 12 ? w4[2] : w4[3]);
-                                if (((wv >> (8 * (x & 3))) & 0x7fu) == 0x7fu) atomicMin(&nm.first[16 * ch + x], b * kStep + row);
-                            }
-                            nm.any = 1;
-#pragma unroll
-                            for (int x = 0; x < 4; ++x) w4[x] &= ~((nan_bytes(w4[x]) >> 7) * 0xffu);
+                        for (int u = 0; u < kConvRows; ++u) {  // rows r0 + 4 u + row8
+                            raw[u] = *reinterpret_cast<const uint4*>(src + (r0 + 4 * u) * 128 + ((ch ^ (4 * (u & 1) + row8)) << 4));
+                            odd |= nan_bytes(raw[u].x) | nan_bytes(raw[u].y) | nan_bytes(raw[u].z) | nan_bytes(raw[u].w);
                         }
-                        uint4 o[2];
-                        o[0] = make_uint4(cvt_e4m3x2(w4[0]), cvt_e4m3x2(w4[0] >> 16), cvt_e4m3x2(w4[1]),
-                                          cvt_e4m3x2(w4[1] >> 16));
-                        o[1] = make_uint4(cvt_e4m3x2(w4[2]), cvt_e4m3x2(w4[2] >> 16), cvt_e4m3x2(w4[3]),
-                                          cvt_e4m3x2(w4[3] >> 16));
-                        // 64 columns in each half; lanes of the two halves store their chunks in
-                        // opposite order, so a quarter warp's eight stores meet different banks
-                        const bool hi = ch >= 4;
-                        uint8_t* line = dst + (hi ? kTile : 0) + row * 128;
-                        const int c0 = 2 * (ch & 3) + (hi ? 1 : 0), c1 = c0 ^ 1;
-                        *reinterpret_cast<uint4*>(line + ((c0 ^ (row & 7)) << 4)) = hi ? o[1] : o[0];
-                        *reinterpret_cast<uint4*>(line + ((c1 ^ (row & 7)) << 4)) = hi ? o[0] : o[1];
-                    }
+                        if (!whole || __any_sync(0xffffffffu, odd != 0u)) {
+#pragma unroll
+                            for (int u = 0; u < kConvRows; ++u) {
+                                const int row = r0 + 4 * u + row8;
+                                uint32_t w4[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+                                if (row >= here || !((valid >> (row / T)) & 1u)) w4[0] = w4[1] = w4[2] = w4[3] = 0u;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const uint32_t bad = nan_bytes(w4[e]);
+                                    if (bad) {
+#pragma unroll 1
+                                        for (int x = 0; x < 4; ++x)
+                                            if ((bad >> (8 * x)) & 0x80u)
+                                                atomicMin(&nm.first[16 * ch + 4 * e + x], b * kStep + row);
+                                        nm.any = 1;
+                                        w4[e] &= ~((bad >> 7) * 0xffu);
+                                    }
+                                }
+                                raw[u] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+                            }
+                        }
+#pragma unroll
+                        for (int u = 0; u < kConvRows; ++u) {
+                            const uint4 o0 = make_uint4(cvt_e4m3x2(raw[u].x), cvt_e4m3x2(raw[u].x >> 16),
+                                                        cvt_e4m3x2(raw[u].y), cvt_e4m3x2(raw[u].y >> 16));
+                            const uint4 o1 = make_uint4(cvt_e4m3x2(raw[u].z), cvt_e4m3x2(raw[u].z >> 16),
+                                                        cvt_e4m3x2(raw[u].w), cvt_e4m3x2(raw[u].w >> 16));
+                            // 64 columns in each half; lanes of the two halves store their chunks in
+                            // opposite order, so a quarter warp's eight stores meet different banks
+                            const bool hi = ch >= 4;
+                            uint8_t* line = dst + (hi ? kTile : 0) + (r0 + 4 * u) * 128;
+                            const int c0 = (2 * (ch & 3) + (hi ? 1 : 0)) ^ (4 * (u & 1) + row8);
+                            *reinterpret_cast<uint4*>(line + (c0 << 4)) = hi ? o1 : o0;
+                            *reinterpret_cast<uint4*>(line + ((c0 ^ 1) << 4)) = hi ? o0 : o1;
+                        }
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -587,18 +618,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else {
-        regs_increase<kSoftmaxRegs>();
         // ======================================================== softmax, epilogue
         const int w = warp >> 2, wq = warp & 3, r = wq * 32 + lane;
         const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
         const uint32_t s_addr = tmem + lane_base + kColS + 128u * w, o_addr = tmem + lane_base + kColO + 128u * w;
         uint32_t it = 0, use = 0, segs = 0;
         bool ok = true;
-        while (ok && wk.next(p, sg)) {
+        while (ok && ww.next(p, lane)) {
             const NanMarks& nm = marks[segs % kMarks];
             const bool first_seg = segs == 0;
             ++segs;
-            const Request& q = wk.it.q;
             const int row0 = sg.tile * kItemRows + w * kTileRows;  // of the warpgroup, in (query, head) order
             const int rows = min(kTileRows, wk.it.rows - row0);
             if (rows <= 0) {  // an empty row tile: the warpgroup reports its place in the walk and waits
@@ -610,162 +639,249 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool on = r < rows;
             const int x = row0 + (on ? r : rows - 1), qi = x / g, j = x - qi * g;
             // tokens this row sees, and the warpgroup's first row
-            const int vis = wk.it.ok ? q.len - q.n + qi + 1 : 0;
-            const int vis_all = wk.it.ok ? q.len - q.n + row0 / g + 1 : 0;
-            // ---- Q: high and low E4M3 parts of the row, its score factor
-            float rs;
+            const int vis = wk.it.ok ? wk.it.q.len - wk.it.q.n + qi + 1 : 0;
+            const int vis_all = wk.it.ok ? wk.it.q.len - wk.it.q.n + row0 / g + 1 : 0;
+            // ---- Q: high and low E4M3 parts of the warp's rows, each row's score factor.  16 lanes share a
+            // row: 8 elements each.
+            float rs = 0.f;
             {
-                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.Q) +
-                                                                  (size_t)(q.q0 + qi) * p.q_stride +
-                                                                  (size_t)(sg.h * g + j) * kHeadDim);
-                uint4 raw[16];
-                uint32_t top = 0;
+                const uint16_t* q0 = static_cast<const uint16_t*>(p.Q) + (size_t)wk.it.q.q0 * p.q_stride +
+                                     (size_t)(sg.h * g) * kHeadDim + (lane & 15) * 8;
+                uint8_t* qt = smem + Layout::q + w * 2 * kTile + (wq * 32 + (lane >> 4)) * 128;
+#pragma unroll 1
+                for (int i0 = 0; i0 < 16; i0 += 8) {
+                uint4 raw[8];
 #pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                    raw[c] = __ldg(src + c);
-                    const uint32_t w4[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+                for (int u = 0; u < 8; ++u) {
+                    const int i = i0 + u;
+                    const int y = row0 + min(wq * 32 + 2 * i + (lane >> 4), rows - 1), yq = y / g;
+                    raw[u] = __ldg(reinterpret_cast<const uint4*>(q0 + (size_t)yq * p.q_stride + (y - yq * g) * kHeadDim));
+                }
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const int i = i0 + u;
+                    const uint32_t w4[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+                    uint32_t top = 0;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) top = max(top, max((w4[e] << 16) & 0x7f800000u, w4[e] & 0x7f800000u));
-                }
-                const int ex = max((int)(top >> 23) - 127, -100);  // the largest element is in [2^ex, 2^(ex+1))
-                const float up = __uint_as_float((uint32_t)(7 - ex + 127) << 23);
-                rs = p.scale_log2 * __uint_as_float((uint32_t)(ex - 7 + 127) << 23);
-                if (ex == 128) rs = __uint_as_float(0x7fc00000u);  // an infinity or NaN in the row
-                uint8_t* qt = smem + Layout::q + w * 2 * kTile + r * 128;
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    uint32_t hi[4], lo[4];
+                    for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    const int ex = max((int)(top >> 23) - 127, -100);  // the largest element is in [2^ex, 2^(ex+1))
+                    const float up = __uint_as_float((uint32_t)(7 - ex + 127) << 23);
+                    const int mine = __shfl_sync(0xffffffffu, ex, (lane & 1) << 4);  // of row 2 i + (lane & 1)
+                    if ((lane >> 1) == i) {
+                        rs = p.scale_log2 * __uint_as_float((uint32_t)(mine - 7 + 127) << 23);
+                        if (mine == 128) rs = __uint_as_float(0x7fc00000u);  // an infinity or NaN in the row
+                    }
+                    uint32_t hi[2], lo[2];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint4 v = raw[2 * c + (e >> 1)];
-                        const uint32_t a = (e & 1) ? v.z : v.x, bb = (e & 1) ? v.w : v.y;
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t a = w4[2 * e], bb = w4[2 * e + 1];
                         const float y[4] = {__uint_as_float(a << 16) * up, __uint_as_float(a & 0xffff0000u) * up,
                                             __uint_as_float(bb << 16) * up, __uint_as_float(bb & 0xffff0000u) * up};
                         hi[e] = pack_e4m3x4(y[0], y[1], y[2], y[3]);
-                        const uint32_t h01 = cvt_e4m3x2(hi[e]), h23 = cvt_e4m3x2(hi[e] >> 16);
                         float z[4];
-                        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
-                            : "=f"(z[0]), "=f"(z[1])
-                            : "r"(h01));
-                        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
-                            : "=f"(z[2]), "=f"(z[3])
-                            : "r"(h23));
+                        f16x2_to_f32(cvt_e4m3x2(hi[e]), z[0], z[1]);
+                        f16x2_to_f32(cvt_e4m3x2(hi[e] >> 16), z[2], z[3]);
                         lo[e] = pack_e4m3x4(y[0] - z[0], y[1] - z[1], y[2] - z[2], y[3] - z[3]);
                     }
-                    const uint32_t at = (uint32_t)((c ^ (r & 7)) << 4);
-                    *reinterpret_cast<uint4*>(qt + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4*>(qt + kTile + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    const int row7 = (2 * i + (lane >> 4)) & 7, ch = (lane & 15) >> 1;
+                    uint8_t* dst = qt + i * 256 + ((ch ^ row7) << 4) + (lane & 1) * 8;
+                    *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
+                    *reinterpret_cast<uint2*>(dst + kTile) = make_uint2(lo[0], lo[1]);
+                }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(B.qfull(w));
             }
             float m = kNegInf, l = 0.f;
-            for (int b = sg.b0; b < sg.b1; ++b, ++it) {
+            const int b0 = sg.b0, b1 = sg.b1;
+            float2* mass_row = nullptr;  // page weights: this row's sums, rowsw * T / 16 apart per page
+            int mass_pages = 0;
+            if (WEIGHTS && on && wk.it.ok) {
+                const Request& q = wk.it.q;
+                mass_row = p.ws_mass + ((size_t)q.p0 * p.c.Hkv + (size_t)sg.h * q.np) * (T / 16) * ((size_t)p.max_q * g) + x;
+                mass_pages = (q.len + T - 1) / T;
+            }
+            for (int b = b0; b < b1; ++b, ++it) {
                 const uint32_t k = use++;
-                ok = warp_ok(mbar_wait(B.mfull(it % kNM), (it / kNM) & 1, abort_flag, p.err, QUP_ERR_TIMEOUT, lim) &&
-                             mbar_wait(B.sfull(w), k & 1, abort_flag, p.err, QUP_ERR_TIMEOUT, lim));
+                ok = warp_ok(mbar_wait_idle(B.mfull(it % kNM), (it / kNM) & 1, abort_flag, p.err, QUP_ERR_TIMEOUT, lim));
+                if (!ok) break;
+                const StepMeta& sm = meta[it % kNM];
+                const uint32_t valid = sm.valid;
+                const bool plain = valid == (1u << PPS) - 1u && sm.negative == 0u && (b + 1) * kStep <= vis_all;
+                ok = warp_ok(mbar_wait_idle(B.sfull(w), k & 1, abort_flag, p.err, QUP_ERR_TIMEOUT, lim));
                 if (!ok) break;
                 tc_fence_after();
-                const StepMeta& sm = meta[it % kNM];
-                uint32_t sv[kStep];
-                tmem_ld128_wait(s_addr, sv);
-                const uint32_t valid = sm.valid;
+                // The scores are read twice, 32 columns at a time with the next on their way (held in
+                // registers for the whole step they would be spilled).  A step that every row sees whole,
+                // without negative scales, is plain: its loops hold no branch, and they stay rolled, since
+                // a loop unrolled over the step's 128 scores waits for its instructions.
+                uint32_t sa[kCols], sb[kCols];
                 const int seen = vis - b * kStep;  // tokens of the step that the row sees
-                float f[PPS], vl[PPS];
+                // scores of unseen tokens become -inf times the factor's sign; for the maximum products
+                // are turned over where the scale is negative
+                const auto mask = [&](uint32_t (&sv)[kCols], int c, bool turn) {
 #pragma unroll
-                for (int q2 = 0; q2 < PPS; ++q2) {
-                    const float ks = sm.ks[q2];
-                    vl[q2] = sm.vl[q2];
-                    f[q2] = rs * ks;
-                    if (ks < 0.f) {  // the largest score of the page is that of the smallest product
+                    for (int h2 = 0; h2 < kCols / TC; ++h2) {
+                        const int q2 = (c * kCols + h2 * TC) / T;
+                        const bool neg = sm.page[q2].x < 0.f;
+                        const int see = ((valid >> q2) & 1u) ? seen - c * kCols : 0;
+                        const uint32_t unseen = __float_as_uint(neg ? -kNegInf : kNegInf);
 #pragma unroll
-                        for (int t = q2 * T; t < (q2 + 1) * T; ++t) sv[t] ^= 0x80000000u;
-                        f[q2] = -f[q2];
+                        for (int t = h2 * TC; t < (h2 + 1) * TC; ++t) {
+                            if (t >= see) sv[t] = unseen;
+                            if (turn && neg) sv[t] ^= 0x80000000u;
+                        }
                     }
-                    // a scale of 0 keeps a positive factor: -inf times it stays -inf
-                    if (f[q2] < 1e-30f) f[q2] = 1e-30f;
-                }
-                if (valid != (1u << PPS) - 1u || (b + 1) * kStep > vis_all) {
-#pragma unroll
-                    for (int q2 = 0; q2 < PPS; ++q2) {
-                        const int see = ((valid >> q2) & 1u) ? seen - q2 * T : 0;
-#pragma unroll
-                        for (int t = 0; t < T; ++t)
-                            if (t >= see) sv[q2 * T + t] = __float_as_uint(kNegInf);
-                    }
-                }
+                };
+                // a page's factor for this row, log2 of its V scale and one over it
+                const auto page = [&](int q2) {
+                    float4 v = sm.page[q2];
+                    v.x *= rs;
+                    // one of a zero scale stays away from 0, as -inf times it has to be -inf
+                    if (fabsf(v.x) < 1e-30f) v.x = 1e-30f;
+                    return v;
+                };
                 float bm = kNegInf;
+                const auto largest = [&](const uint32_t (&sv)[kCols], int c) {
 #pragma unroll
-                for (int q2 = 0; q2 < PPS; ++q2) {
-                    float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+                    for (int h2 = 0; h2 < kCols / TC; ++h2) {
+                        const float4 pg = page((c * kCols + h2 * TC) / T);
+                        float mx[2] = {kNegInf, kNegInf};
 #pragma unroll
-                    for (int t = q2 * T; t < (q2 + 1) * T; t += 8)
+                        for (int t = h2 * TC; t < (h2 + 1) * TC; t += 4)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            mx[e] = max3f(mx[e], __uint_as_float(sv[t + 2 * e]), __uint_as_float(sv[t + 2 * e + 1]));
-                    bm = fmaxf(bm, fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), f[q2], vl[q2]));
+                            for (int e = 0; e < 2; ++e)
+                                mx[e] = max3_nan(mx[e], __uint_as_float(sv[t + 2 * e]), __uint_as_float(sv[t + 2 * e + 1]));
+                        bm = max3_nan(bm, fmaf(mx[0], fabsf(pg.x), pg.y), fmaf(mx[1], fabsf(pg.x), pg.y));
+                    }
+                };
+                if (plain) {
+                    tmem_ld32(s_addr, sa);
+#pragma unroll 1
+                    for (int c = 0; c < kStep / kCols; c += 2) {
+                        tmem_wait_ld();
+                        reg_fence<kCols>(sa);
+                        tmem_ld32(s_addr + kCols * (c + 1), sb);
+                        largest(sa, c);
+                        tmem_wait_ld();
+                        reg_fence<kCols>(sb);
+                        tmem_ld32(s_addr + (c + 2) % (kStep / kCols) * kCols, sa);
+                        largest(sb, c + 1);
+                    }
+                    tmem_wait_ld();
+                    reg_fence<kCols>(sa);
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < kStep / kCols; ++c) {
+                        tmem_ld32_wait(s_addr + kCols * c, sa);
+                        mask(sa, c, true);
+                        largest(sa, c);
+                    }
                 }
-                const bool mv = bm > m + kLazy;
+                const bool mv = !(bm <= m + kLazy);  // or NaN, which then stays
                 if (__any_sync(0xffffffffu, mv)) {
                     const float a = mv ? ex2(m - bm) : 1.f;
                     if (mv) m = bm;
                     l *= a;
                     // S(b) was issued after the last O update had finished: O is free to be rescaled
-                    if (b > sg.b0) {
+                    if (b > b0) {
 #pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
+                        for (int c = 0; c < 8; ++c) {
                             uint32_t ov[32];
-                            tmem_ld32_wait(o_addr + 32u * c, ov);
+                            tmem_ld16(o_addr + 16u * c, ov);
+                            tmem_wait_ld();
+                            reg_fence<16>(ov);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * a);
-                            tmem_st_x32(o_addr + 32u * c, ov);
+                            for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * a);
+                            tmem_st16(o_addr + 16u * c, ov);
                         }
                     }
                 }
                 const float sub = m == kNegInf ? 0.f : m - kOffset;
+                float mass = 0.f;  // of the page so far
+                // P of 16 tokens (from token t1 of the step, at sv) takes 8 columns, of scores that have
+                // been read
+                const auto exps = [&](const uint32_t* sv, int t1, const float4& pg) {
+                    const f2 f2f{pg.x, pg.x}, off{pg.y - sub, pg.y - sub};
+                    f2 e[8];
 #pragma unroll
-                for (int q2 = 0; q2 < PPS; ++q2) {
-                    const f2 ff{f[q2], f[q2]}, off{vl[q2] - sub, vl[q2] - sub};
-                    f2 part[2] = {{0.f, 0.f}, {0.f, 0.f}};
-                    uint32_t ck[8];
-#pragma unroll
-                    for (int t = q2 * T; t < (q2 + 1) * T; t += 2) {
-                        f2 e = fma2(f2{__uint_as_float(sv[t]), __uint_as_float(sv[t + 1])}, ff, off);
-                        e.x = ex2(e.x);
-                        e.y = ex2(e.y);
-                        part[(t >> 1) & 1] = add2(part[(t >> 1) & 1], e);
-                        ck[(t & 15) >> 1] = pack_f16x2(e.x, e.y);
-                        if ((t & 15) == 14) tmem_st_x8(s_addr + (uint32_t)(t >> 1) - 7u, ck);
-                    }
-                    const f2 ps = add2(part[0], part[1]);
-                    const float mass = (ps.x + ps.y) * sm.vi[q2];
-                    l += mass;
-                    if constexpr (WEIGHTS) {
-                        const int pg = b * PPS + q2;
-                        if (on && (long long)pg * T < q.len && wk.it.ok) {
-                            const size_t rowsw = (size_t)p.max_q * g;
-                            p.ws_mass[((size_t)q.p0 * p.c.Hkv + (size_t)sg.h * q.np + pg) * (T / 16) * rowsw + x] =
-                                make_float2(mass, m);
+                    for (int i = 0; i < 8; ++i) {
+                        e[i] = fma2(f2{__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])}, f2f, off);
+                        if (i < kPolyPairs) {
+                            e[i] = exp2_poly2q(e[i]);
+                        } else {
+                            e[i].x = ex2(e[i].x);
+                            e[i].y = ex2(e[i].y);
                         }
                     }
+                    uint32_t ck[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) ck[i] = pack_f16x2(e[i].x, e[i].y);
+                    tmem_st_x8(s_addr + (uint32_t)(t1 >> 1), ck);
+                    const f2 ps = add2(add2(add2(e[0], e[1]), add2(e[2], e[3])), add2(add2(e[4], e[5]), add2(e[6], e[7])));
+                    const float sum = (ps.x + ps.y) * pg.z;
+                    l += sum;
+                    if constexpr (WEIGHTS) {
+                        mass += sum;
+                        if ((t1 + 16) % T == 0) {
+                            const int pg = b * PPS + t1 / T;
+                            if (pg < mass_pages)
+                                mass_row[(size_t)pg * (T / 16) * ((size_t)p.max_q * g)] = make_float2(mass, m);
+                            mass = 0.f;
+                        }
+                    }
+                };
+                const auto signal = [&](int half) {  // half a step of P is there for the O update
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(B.pfull(w, half));
+                };
+                if (plain) {  // the first 16 scores are there
+                    float4 pa = page(0);
+#pragma unroll 1
+                    for (int t1 = 0; t1 < kStep; t1 += 32) {
+                        tmem_ld16(s_addr + t1 + 16, sb);
+                        const float4 pb = T < 32 ? page((t1 + 16) / T) : pa;
+                        exps(sa, t1, pa);
+                        tmem_wait_ld();
+                        reg_fence<16>(sb);
+                        tmem_ld16(s_addr + (t1 + 32) % kStep, sa);
+                        if (T < kStep) pa = page((t1 + 32) % kStep / T);
+                        exps(sb, t1 + 16, pb);
+                        tmem_wait_ld();
+                        reg_fence<16>(sa);
+                        if (t1 & 32) signal(t1 >> 6);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < kStep / kCols; ++c) {
+                        tmem_ld32_wait(s_addr + kCols * c, sa);
+                        mask(sa, c, false);
+                        exps(sa, c * kCols, page(c * kCols / T));
+                        exps(sa + 16, c * kCols + 16, page((c * kCols + 16) / T));
+                        if (c & 1) signal(c >> 1);
+                    }
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(B.pfull(w));
             }
             if (!ok) break;
             // ---- the row's result, or its part of it
-            ok = warp_ok(mbar_wait(B.pvdone(w), (use - 1) & 1, abort_flag, p.err, QUP_ERR_TIMEOUT, lim));
+            ok = warp_ok(mbar_wait_idle(B.pvdone(w), (use - 1) & 1, abort_flag, p.err, QUP_ERR_TIMEOUT, lim));
             if (!ok) break;
             tc_fence_after();
-            const bool complete = sg.b0 == 0 && sg.b1 == sg.steps;
+            const bool complete = b0 == 0 && b1 == sg.steps;
             const size_t part = (size_t)2 * blockIdx.x + (first_seg ? 0 : 1);
-            const size_t prow = part * kItemRows + w * kTileRows + r;
-            const size_t at = (size_t)(q.q0 + qi) * p.Hq + sg.h * g + j;
+            const size_t prow0 = part * kItemRows + w * kTileRows + wq * 32;
+            const size_t q0 = (size_t)wk.it.q.q0;
+            const size_t at = (q0 + qi) * p.Hq + sg.h * g + j;
             const bool nan = *reinterpret_cast<const volatile int*>(&nm.any) != 0;
             const float inv = l == 0.f ? 0.f : __fdividef(1.f, l);
+            // 32 columns at a time through the warp's rows of the Q tile (every S that reads them is done),
+            // so that a row's 128 (partial results) or 64 bytes leave as one piece
+            uint8_t* stage = smem + Layout::q + w * 2 * kTile + wq * 32 * 128;
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
                 uint32_t ov[32];
@@ -775,9 +891,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int e = 0; e < 32; ++e)
                         if (nm.first[32 * c + e] < vis) ov[e] = 0x7fc00000u;
                 }
-                if (!on) continue;
+                __syncwarp();
                 if (complete) {
-                    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.O) + at * kHeadDim + 32 * c);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         uint32_t o[4];
@@ -785,32 +900,54 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int y = 0; y < 4; ++y)
                             o[y] = pack_bf16x2(__uint_as_float(ov[8 * e + 2 * y]) * inv,
                                                __uint_as_float(ov[8 * e + 2 * y + 1]) * inv);
-                        dst[e] = make_uint4(o[0], o[1], o[2], o[3]);
+                        *reinterpret_cast<uint4*>(stage + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4)) =
+                            make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {  // 8 rows, 4 lanes each
+                        const int rr = 8 * i + (lane >> 2);
+                        const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4));
+                        if (wq * 32 + rr < rows) {
+                            const int y = row0 + wq * 32 + rr, yq = y / g;
+                            const size_t to = (q0 + yq) * p.Hq + sg.h * g + (y - yq * g);
+                            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.O) + to * kHeadDim + 32 * c + (lane & 3) * 8) = v;
+                        }
                     }
                 } else {
-                    uint4* dst = reinterpret_cast<uint4*>(p.chunk_o + prow * kHeadDim + 32 * c);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) dst[e] = make_uint4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
+                    for (int e = 0; e < 8; ++e)
+                        *reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+                            make_uint4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {  // 4 rows, 8 lanes each
+                        const int rr = 4 * i + (lane >> 3);
+                        const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
+                        if (wq * 32 + rr < rows)
+                            *reinterpret_cast<uint4*>(p.chunk_o + (prow0 + rr) * kHeadDim + 32 * c + (lane & 7) * 4) = v;
+                    }
                 }
             }
+            __syncwarp();
             if (on) {
                 if (complete) {
                     const float l2 = l == 0.f ? kNegInf : m - kOffset + lg2(l);
                     if (p.lse) p.lse[at] = l2 * 0.69314718055994531f;
                     if (WEIGHTS) p.ws_lse[at] = l2;
                 } else {
-                    p.chunk_ml[prow] = make_float2(m, l);
+                    p.chunk_ml[prow0 + lane] = make_float2(m, l);
                 }
             }
             // warpgroup 1 takes part in every phase of this barrier (see the empty row tile)
-            if (w == 1) ok = warp_ok(mbar_wait(B.sdone(), (segs - 1) & 1, abort_flag, p.err, QUP_ERR_TIMEOUT, lim));
+            if (w == 1) ok = warp_ok(mbar_wait_idle(B.sdone(), (segs - 1) & 1, abort_flag, p.err, QUP_ERR_TIMEOUT, lim));
         }
     }
 
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == kSWarp) tmem_dealloc(tmem, 512);
+    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
 // ------------------------------------------------------------------ join of cut items
@@ -865,12 +1002,6 @@ template <int T, bool WEIGHTS>
 cudaError_t launch_t(const CUtensorMap& tmK, const CUtensorMap& tmV, const CacheAttnParams& p, int runs,
                      cudaStream_t stream) {
     const auto kernel = cache_chunk_kernel<T, WEIGHTS>;
-    // an increase beyond the launch's registers would never be granted: no other count is launched
-    static const int regs = [] {
-        cudaFuncAttributes a;
-        return cudaFuncGetAttributes(&a, (const void*)cache_chunk_kernel<T, WEIGHTS>) == cudaSuccess ? a.numRegs : -1;
-    }();
-    if (regs != kLaunchRegs) return cudaErrorInvalidConfiguration;
     const size_t smem = cache_chunk_smem();
     cudaError_t e = ensure_smem_attr((const void*)kernel, smem);
     if (e != cudaSuccess) return e;
