@@ -466,12 +466,22 @@ def _need(ok, what: str):
         raise ValueError(what)
 
 
-def _whole(t, name: str, dtype, shape, device):
-    """t is a contiguous tensor of this type and shape on this device."""
-    _need(t.dtype == dtype, f"{name}: {dtype} wanted, got {t.dtype}")
-    _need(tuple(t.shape) == tuple(shape), f"{name}: shape {tuple(shape)} wanted, got {tuple(t.shape)}")
-    _need(t.is_contiguous(), f"{name} is not contiguous")
-    _need(t.device == device, f"{name} is on {t.device}, the cache on {device}")
+def _whole(t, name: str, dtype, shape, index: int):
+    """t is a contiguous tensor of this type and shape on device `index`.  The message is put together only
+    when it is needed: these checks are most of what a short call costs on the host."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == index:
+        return
+    raise ValueError(f"{name}: contiguous {dtype} {tuple(shape)} on device {index} wanted, got {t.dtype} "
+                     f"{tuple(t.shape)} with strides {t.stride()} on {t.device}")
+
+
+def _heads(t, name: str, dtype, shape, index: int):
+    """As _whole, but with any stride between the rows of the first dimension."""
+    if (t.dtype is dtype and t.shape == shape and t.get_device() == index and
+            (t.is_contiguous() or (t.stride(2) == 1 and t.stride(1) == 128))):
+        return
+    raise ValueError(f"{name}: {dtype} {tuple(shape)} with contiguous heads on device {index} wanted, got {t.dtype} "
+                     f"{tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
 
 class KVCache:
@@ -486,42 +496,53 @@ class KVCache:
     the page table is rewritten by cache_evict), the tensors may not be replaced.
     """
 
-    __slots__ = ("K", "V", "k_scale", "v_scale", "page_table", "page_ptr", "kv_len", "max_pages", "device", "_c",
-                 "_ref")
+    __slots__ = ("K", "V", "k_scale", "v_scale", "page_table", "page_ptr", "kv_len", "max_pages", "device", "R", "Hkv",
+                 "total_pages", "_c", "_ref", "_index")
 
     def __init__(self, K, V, k_scale, v_scale, page_table, page_ptr, kv_len, max_pages: Optional[int] = None):
         import torch
         _need(K.dim() == 4 and K.shape[3] == 128, f"K: [P_phys][Hkv][T][128] wanted, got {tuple(K.shape)}")
         P_phys, Hkv, T, _ = K.shape
-        dev = K.device
+        index = K.get_device()
         _need(K.dtype in (torch.uint8, torch.float8_e4m3fn), f"K: uint8 or float8_e4m3fn wanted, got {K.dtype}")
         for t, name in ((K, "K"), (V, "V")):
-            _whole(t, name, K.dtype, K.shape, dev)
+            _whole(t, name, K.dtype, K.shape, index)
         for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-            _whole(t, name, torch.float32, (P_phys, Hkv), dev)
+            _whole(t, name, torch.float32, (P_phys, Hkv), index)
         for t, name in ((page_table, "page_table"), (page_ptr, "page_ptr"), (kv_len, "kv_len")):
-            _whole(t, name, torch.int32, (t.numel(),), dev)
+            _whole(t, name, torch.int32, (t.numel(),), index)
         _need(page_ptr.numel() == kv_len.numel() + 1, "page_ptr has one entry more than kv_len")
         _need(T in (16, 32, 64, 128), f"page size {T}: 16, 32, 64 or 128 wanted")
         _need(page_table.numel() > 0 and P_phys > 0, "an empty page table or cache")
         if max_pages is None:
             max_pages = page_table.numel()
         _need(1 <= max_pages <= page_table.numel(), f"max_pages {max_pages}: 1 .. {page_table.numel()} wanted")
-        _need(dev.type == "cuda", f"the cache is on {dev}: CUDA tensors wanted")
+        _need(K.is_cuda, f"the cache is on {K.device}: CUDA tensors wanted")
         self.K, self.V, self.k_scale, self.v_scale = K, V, k_scale, v_scale
         self.page_table, self.page_ptr, self.kv_len = page_table, page_ptr, kv_len
-        self.max_pages, self.device = max_pages, dev
+        self.max_pages, self.device, self._index = max_pages, K.device, index
+        self.R, self.Hkv, self.total_pages = kv_len.numel(), Hkv, page_table.numel()
         self._c = _CacheStruct(*[t.data_ptr() for t in (K, V, k_scale, v_scale, page_table, page_ptr, kv_len)],
-                               P_phys, Hkv, T, kv_len.numel(), page_table.numel(), max_pages)
+                               P_phys, Hkv, T, self.R, self.total_pages, max_pages)
         self._ref = ctypes.byref(self._c)
 
 
-def _on(cache: KVCache, stream):
-    """The device the call runs on, and its stream (default: that device's current one)."""
+def _launch(fn, where: str, index: int, stream, *args):
+    """fn(*args, stream) with the cache's device current; stream: a torch stream, or None for that device's
+    current one."""
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream(cache.device)
-    _need(s.device == cache.device, f"the stream is on {s.device}, the cache on {cache.device}")
-    return torch.cuda.device(cache.device), ctypes.c_void_p(s.cuda_stream)
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        _need(stream.device.index == index, f"the stream is on {stream.device}, the cache on device {index}")
+        raw = stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, raw)
+    if rc != 0:
+        raise QupError(rc, where)
 
 
 def cache_append(cache: KVCache, k_new, v_new, tok_ptr, stream=None):
@@ -533,21 +554,16 @@ def cache_append(cache: KVCache, k_new, v_new, tok_ptr, stream=None):
     requantised).
     """
     import torch
-    c = cache._c
-    _need(k_new.dtype in (torch.bfloat16, torch.float32), f"k_new: bfloat16 or float32 wanted, got {k_new.dtype}")
-    for t, name in ((k_new, "k_new"), (v_new, "v_new")):
-        _need(t.dtype == k_new.dtype and t.dim() == 3 and t.shape == k_new.shape and t.shape[1:] == (c.Hkv, 128),
-              f"{name}: [N][{c.Hkv}][128] of {k_new.dtype} wanted, got {tuple(t.shape)} of {t.dtype}")
-        _need(t.shape[0] == 0 or (t.stride(2) == 1 and t.stride(1) == 128), f"{name}: a token's heads are not contiguous")
-        _need(t.device == cache.device, f"{name} is on {t.device}, the cache on {cache.device}")
-    _whole(tok_ptr, "tok_ptr", torch.int32, (c.R + 1,), cache.device)
-    N, least = k_new.shape[0], c.Hkv * 128
-    ks, vs = (k_new.stride(0), v_new.stride(0)) if N > 1 else (least, least)
-    guard, st = _on(cache, stream)
-    with guard:
-        _check(load().qup_cache_append(cache._ref, k_new.data_ptr(), v_new.data_ptr(),
-                                       BF16 if k_new.dtype == torch.bfloat16 else F32, ks, vs, tok_ptr.data_ptr(), N,
-                                       128, st), "qup_cache_append")
+    index, hkv, dtype = cache._index, cache.Hkv, k_new.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise ValueError(f"k_new: bfloat16 or float32 wanted, got {dtype}")
+    N = k_new.shape[0]
+    _heads(k_new, "k_new", dtype, (N, hkv, 128), index)
+    _heads(v_new, "v_new", dtype, (N, hkv, 128), index)
+    _whole(tok_ptr, "tok_ptr", torch.int32, (cache.R + 1,), index)
+    ks, vs = (k_new.stride(0), v_new.stride(0)) if N > 1 else (hkv * 128, hkv * 128)
+    _launch((_lib or load()).qup_cache_append, "qup_cache_append", index, stream, cache._ref, k_new.data_ptr(),
+            v_new.data_ptr(), BF16 if dtype is torch.bfloat16 else F32, ks, vs, tok_ptr.data_ptr(), N, 128)
 
 
 def cache_attn_workspace(cache: KVCache, Nq: int, Hq: int, max_q: int, page_weight: bool = False):
@@ -570,38 +586,34 @@ def cache_attn(cache: KVCache, Q, q_ptr, max_q: int, topk=None, softmax_scale: O
     [total_pages][Hkv] if given.  Returns O [Nq][Hq][128] bf16.
     """
     import torch
-    c, dev = cache._c, cache.device
-    _need(Q.dtype == torch.bfloat16 and Q.dim() == 3 and Q.shape[2] == 128,
-          f"Q: [Nq][Hq][128] of bfloat16 wanted, got {tuple(Q.shape)} of {Q.dtype}")
-    Nq, Hq, _ = Q.shape
-    _need(Nq == 0 or (Q.stride(2) == 1 and Q.stride(1) == 128), "Q: a query's heads are not contiguous")
-    _need(Q.device == dev, f"Q is on {Q.device}, the cache on {dev}")
-    _whole(q_ptr, "q_ptr", torch.int32, (c.R + 1,), dev)
-    ksel = 0
+    index = cache._index
+    _need(Q.dim() == 3, "Q: [Nq][Hq][128] wanted")
+    Nq, Hq, _ = shape = Q.shape
+    _heads(Q, "Q", torch.bfloat16, (Nq, Hq, 128), index)
+    _whole(q_ptr, "q_ptr", torch.int32, (cache.R + 1,), index)
+    ksel = topk_p = lse_p = weight_p = None
     if topk is not None:
         ksel = topk.shape[-1]
-        _whole(topk, "topk", torch.int32, (Hq, Nq, ksel), dev)
+        _whole(topk, "topk", torch.int32, (Hq, Nq, ksel), index)
+        topk_p = topk.data_ptr()
     if out is None:
-        out = torch.empty(Q.shape, dtype=Q.dtype, device=dev)
+        out = torch.empty(shape, dtype=torch.bfloat16, device=Q.device)
     else:
-        _whole(out, "out", torch.bfloat16, Q.shape, dev)
+        _whole(out, "out", torch.bfloat16, shape, index)
     if lse is not None:
-        _whole(lse, "lse", torch.float32, (Nq, Hq), dev)
+        _whole(lse, "lse", torch.float32, (Nq, Hq), index)
+        lse_p = lse.data_ptr()
     if page_weight is not None:
-        _whole(page_weight, "page_weight", torch.float32, (c.total_pages, c.Hkv), dev)
+        _whole(page_weight, "page_weight", torch.float32, (cache.total_pages, cache.Hkv), index)
+        weight_p = page_weight.data_ptr()
     if workspace is None:
         workspace = cache_attn_workspace(cache, Nq, Hq, max_q, page_weight is not None)
-    else:
-        _whole(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
-    if softmax_scale is None:
-        softmax_scale = 1.0 / math.sqrt(128)
-    guard, st = _on(cache, stream)
-    with guard:
-        _check(load().qup_cache_attn(cache._ref, Q.data_ptr(), Q.stride(0) if Nq > 1 else Hq * 128, q_ptr.data_ptr(),
-                                     Nq, max_q, Hq, 128, None if topk is None else topk.data_ptr(), ksel,
-                                     softmax_scale, out.data_ptr(), None if lse is None else lse.data_ptr(),
-                                     None if page_weight is None else page_weight.data_ptr(), workspace.data_ptr(),
-                                     workspace.numel(), st), "qup_cache_attn")
+    size = workspace.numel()
+    _whole(workspace, "workspace", torch.uint8, (size,), index)
+    _launch((_lib or load()).qup_cache_attn, "qup_cache_attn", index, stream, cache._ref, Q.data_ptr(),
+            Q.stride(0) if Nq > 1 else Hq * 128, q_ptr.data_ptr(), Nq, max_q, Hq, 128, topk_p, ksel or 0,
+            1.0 / math.sqrt(128) if softmax_scale is None else softmax_scale, out.data_ptr(), lse_p, weight_p,
+            workspace.data_ptr(), size)
     return out
 
 
@@ -616,23 +628,20 @@ def cache_evict(cache: KVCache, page_weight, acc, budget: int, sink: int = 1, re
     four tensors if given, which may be the cache's own page_table and kv_len, and acc.
     """
     import torch
-    c, dev = cache._c, cache.device
-    _whole(page_weight, "page_weight", torch.float32, (c.total_pages, c.Hkv), dev)
-    _whole(acc, "acc", torch.float32, (c.total_pages,), dev)
+    index, n = cache._index, cache.total_pages
+    _whole(page_weight, "page_weight", torch.float32, (n, cache.Hkv), index)
+    _whole(acc, "acc", torch.float32, (n,), index)
     if out is None:
         out = (torch.empty_like(cache.page_table), torch.empty_like(acc), torch.empty_like(cache.kv_len),
                torch.empty_like(cache.page_table))
-    else:
-        for t, name, dtype, n in zip(out, ("page_table", "acc", "kv_len", "page_src"),
-                                     (torch.int32, torch.float32, torch.int32, torch.int32),
-                                     (c.total_pages, c.total_pages, c.R, c.total_pages)):
-            _whole(t, "out " + name, dtype, (n,), dev)
     table, acc_out, lens, src = out
-    guard, st = _on(cache, stream)
-    with guard:
-        _check(load().qup_cache_evict(cache._ref, page_weight.data_ptr(), acc.data_ptr(), decay, budget, sink, recent,
-                                      table.data_ptr(), acc_out.data_ptr(), lens.data_ptr(), src.data_ptr(), st),
-               "qup_cache_evict")
+    _whole(table, "out page_table", torch.int32, (n,), index)
+    _whole(acc_out, "out acc", torch.float32, (n,), index)
+    _whole(lens, "out kv_len", torch.int32, (cache.R,), index)
+    _whole(src, "out page_src", torch.int32, (n,), index)
+    _launch((_lib or load()).qup_cache_evict, "qup_cache_evict", index, stream, cache._ref, page_weight.data_ptr(),
+            acc.data_ptr(), decay, budget, sink, recent, table.data_ptr(), acc_out.data_ptr(), lens.data_ptr(),
+            src.data_ptr())
     return table, acc_out, lens, src
 
 

@@ -57,8 +57,8 @@ __device__ __forceinline__ Request load_request(const int32_t* row_ptr, int N, c
 }
 
 cudaError_t launch_cache_append(const CacheView& c, const void* k_new, const void* v_new, bool bf16,
-                                long long k_stride, long long v_stride, const int32_t* tok_ptr, int N, unsigned* err,
-                                cudaStream_t stream);
+                                long long k_stride, long long v_stride, const int32_t* tok_ptr, int N, int sms,
+                                unsigned* err, cudaStream_t stream);
 
 // At most kMaxEvictPages used pages of one request (a CTA's shared memory holds them).
 constexpr int kMaxEvictPages = 24576;

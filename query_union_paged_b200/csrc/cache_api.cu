@@ -17,7 +17,7 @@ namespace {
 constexpr int kMaxSparseRows = 32;  // Q heads of a KV head in a TopK call: bits of a page's row mask
 
 int check_cache(const qup_cache* c) {
-    if (!c || c->P_phys <= 0 || c->Hkv <= 0 || c->Hkv > 65535 || c->R < 0 || c->total_pages <= 0) return QUP_ERR_ARG;
+    if (!c || c->P_phys <= 0 || c->Hkv <= 0 || c->Hkv > 32767 || c->R < 0 || c->total_pages <= 0) return QUP_ERR_ARG;
     if (!(c->T == 16 || c->T == 32 || c->T == 64 || c->T == 128)) return QUP_ERR_ARG;
     if (c->max_pages < 1 || c->max_pages > c->total_pages) return QUP_ERR_ARG;
     if ((int64_t)c->max_pages * c->T >= ((int64_t)1 << 31)) return QUP_ERR_ARG;  // token positions are int32
@@ -106,11 +106,11 @@ int qup_cache_append(const qup_cache* cache, const void* k_new, const void* v_ne
     if (N == 0 || cache->R == 0) return QUP_OK;
     if (check_cache_pointers(cache) || !k_new || !v_new || !tok_ptr) return QUP_ERR_ARG;
     if ((reinterpret_cast<uintptr_t>(k_new) | reinterpret_cast<uintptr_t>(v_new)) & 15) return QUP_ERR_ARG;
-    if ((int64_t)N / cache->T + 2 * (int64_t)cache->R >= ((int64_t)1 << 31)) return QUP_ERR_ARG;
+    if ((int64_t)N / cache->T + 2 * (int64_t)cache->R >= ((int64_t)1 << 31) - 1) return QUP_ERR_ARG;
     qup::DeviceInfo dev;
     if ((rc = qup::device_info(&dev))) return rc;
     return qup::launch_cache_append(view_of(cache), k_new, v_new, dtype == QUP_BF16, k_stride, v_stride, tok_ptr, N,
-                                    dev.err, static_cast<cudaStream_t>(stream)) == cudaSuccess
+                                    dev.sms, dev.err, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? QUP_OK
                : QUP_ERR_CUDA;
 }

@@ -7,10 +7,11 @@
 // of the exponent (only values that become subnormal are rounded again), so a page filled one token
 // at a time holds the bytes of a page written at once, but for those.
 //
-// One CTA per (run of a request's tokens inside one page, KV head, K or V): the run's tokens are
-// read once into registers (16 bytes of bf16 a load), their largest finite magnitude is reduced over the CTA, and
-// the registers are scaled, rounded (nearest even) and written.  Bound by DRAM: N * Hkv * 128 *
-// (element + 1) bytes for each of K and V.
+// One CTA per run of a request's tokens inside one page, for some of its units (K or V of a KV head).  A
+// unit's tokens are read once into registers (16 bytes a load), their largest finite magnitude is
+// reduced over the CTA, and the registers are scaled, rounded (nearest even) and written; the next
+// unit's loads are under way meanwhile.  Bound by DRAM: N * Hkv * 128 * (element + 1) bytes for each of
+// K and V.
 #include <algorithm>
 #include <cstdint>
 
@@ -22,7 +23,6 @@
 namespace qup {
 namespace {
 
-constexpr int kAppendThreads = 256;
 constexpr int kChunk = 8;                        // elements of one thread's load
 constexpr int kChunksPerToken = kHeadDim / kChunk;
 
@@ -60,21 +60,25 @@ __device__ __forceinline__ uint32_t pack_e4m3_checked(const float* x) {
     return w;
 }
 
+template <int T>
+constexpr int kAppendThreads = T == 128 ? 512 : 256;
+
 template <int T, bool BF16>
-__global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(CacheView c, const void* __restrict__ k_new,
-                                                                      const void* __restrict__ v_new,
-                                                                      long long k_stride, long long v_stride,
-                                                                      const int32_t* __restrict__ tok_ptr, int N,
-                                                                      unsigned* err) {
-    constexpr int CH = T * kChunksPerToken / kAppendThreads;  // chunks of one thread
+__global__ void __launch_bounds__(kAppendThreads<T>) cache_append_kernel(CacheView c, const void* __restrict__ k_new,
+                                                                           const void* __restrict__ v_new,
+                                                                           long long k_stride, long long v_stride,
+                                                                           const int32_t* __restrict__ tok_ptr, int N,
+                                                                           int units, unsigned* err) {
+    constexpr int NT = kAppendThreads<T>;
+    constexpr int CH = T * kChunksPerToken / NT;  // chunks of one thread
+    constexpr int W = BF16 ? 1 : 2;               // 16-byte words of a chunk
     __shared__ int s_req;
-    __shared__ uint32_t s_max[kAppendThreads / 32];
-    const int tid = threadIdx.x, item = blockIdx.x, h = blockIdx.y;
-    const bool isv = blockIdx.z != 0;
+    __shared__ uint32_t s_max[2][NT / 32];
+    const int tid = threadIdx.x, item = blockIdx.x;
     grid_dep_wait();
     if (tid == 0) s_req = -1;
     __syncthreads();
-    for (int r = tid; r < c.R; r += kAppendThreads)
+    for (int r = tid; r < c.R; r += NT)
         if (item_start(tok_ptr[r], r, T) <= item && item < item_start(tok_ptr[r + 1], r + 1, T)) s_req = r;
     __syncthreads();
     const int r = s_req;
@@ -94,119 +98,134 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(CacheView 
         if (tid == 0) atomicOr(err, QUP_ERR_PHYS_PAGE);
         return;
     }
-    float* scale = (isv ? c.v_scale : c.k_scale) + (size_t)phys * c.Hkv + h;
-    const float s_old = a > 0 ? *scale : 0.f;
-    if (!(s_old >= 0.f) || (__float_as_uint(s_old) & 0x7f800000u) == 0x7f800000u) {
-        if (tid == 0) atomicOr(err, QUP_ERR_SCALE);
-        return;
-    }
-    uint8_t* out = (isv ? c.V : c.K) + ((size_t)phys * c.Hkv + h) * T * kHeadDim;
-    const char* in = static_cast<const char*>(isv ? v_new : k_new);
-    const long long stride = isv ? v_stride : k_stride;
-
-    // the run's tokens, and the largest finite magnitude among them
-    uint4 raw[CH][BF16 ? 1 : 2];
-    uint32_t amax = 0;
+    // units (K or V of a head) [u0, u1): the next one's tokens are on their way while one is written
+    const int u0 = blockIdx.y * units, u1 = min(2 * c.Hkv, u0 + units);
+    const auto load = [&](int u, uint4 (&raw)[CH][W]) {
+        const char* in = static_cast<const char*>((u & 1) ? v_new : k_new);
+        const long long stride = (u & 1) ? v_stride : k_stride;
 #pragma unroll
-    for (int u = 0; u < CH; ++u) {
-        const int x = tid + u * kAppendThreads, slot = x / kChunksPerToken, part = x % kChunksPerToken;
-        if (slot < a || slot >= b) continue;
-        const long long at = (tok0 + slot) * stride + (long long)h * kHeadDim + part * kChunk;
-        if constexpr (BF16) {
-            raw[u][0] = __ldg(reinterpret_cast<const uint4*>(in + at * 2));
-            const uint32_t w[4] = {raw[u][0].x, raw[u][0].y, raw[u][0].z, raw[u][0].w};
+        for (int x = 0; x < CH; ++x) {
+            const int at = tid + x * NT, slot = at / kChunksPerToken, part = at % kChunksPerToken;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t lo = (w[e] << 16) & 0x7fffffffu, hi = w[e] & 0x7fff0000u;
-                if (lo < 0x7f800000u) amax = max(amax, lo);
-                if (hi < 0x7f800000u) amax = max(amax, hi);
-            }
-        } else {
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                raw[u][v] = __ldg(reinterpret_cast<const uint4*>(in + at * 4) + v);
-                const uint32_t w[4] = {raw[u][v].x, raw[u][v].y, raw[u][v].z, raw[u][v].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t m = w[e] & 0x7fffffffu;
-                    if (m < 0x7f800000u) amax = max(amax, m);
-                }
+            for (int v = 0; v < W; ++v) {
+                raw[x][v] = make_uint4(0u, 0u, 0u, 0u);
+                if (slot >= a && slot < b)
+                    raw[x][v] = __ldg(reinterpret_cast<const uint4*>(
+                                          in + ((tok0 + slot) * stride + (long long)(u >> 1) * kHeadDim + part * kChunk) *
+                                                   (BF16 ? 2 : 4)) +
+                                      v);
             }
         }
-    }
-    amax = __reduce_max_sync(0xffffffffu, amax);
-    if ((tid & 31) == 0) s_max[tid >> 5] = amax;
-    __syncthreads();
+    };
+    uint4 raw[CH][W], next[CH][W];
+    load(u0, raw);
+    for (int u = u0; u < u1; ++u) {
+        const int h = u >> 1;
+        const bool isv = u & 1;
+        float* scale = (isv ? c.v_scale : c.k_scale) + (size_t)phys * c.Hkv + h;
+        const float s_old = a > 0 ? *scale : 0.f;
+        if (u + 1 < u1) load(u + 1, next);
+        uint8_t* out = (isv ? c.V : c.K) + ((size_t)phys * c.Hkv + h) * T * kHeadDim;
+        // the largest finite magnitude of the run's tokens
+        uint32_t amax = 0;
 #pragma unroll
-    for (int w = 0; w < kAppendThreads / 32; ++w) amax = max(amax, s_max[w]);
-    const float s = fmaxf(pow2(scale_exponent(amax)), s_old);
-    // 1 / s is exact for a power of two; a caller's own scale (s_old kept) takes the division
-    const bool exact = (__float_as_uint(s) & 0x7fffffu) == 0 && s < 8.5e37f;  // 2^126
-    const float inv = exact ? pow2(127 - (int)(__float_as_uint(s) >> 23)) : 0.f;
+        for (int x = 0; x < CH; ++x)
 #pragma unroll
-    for (int u = 0; u < CH; ++u) {
-        const int x = tid + u * kAppendThreads, slot = x / kChunksPerToken, part = x % kChunksPerToken;
-        uint2* dst = reinterpret_cast<uint2*>(out + (size_t)slot * kHeadDim + part * kChunk);
-        float f[kChunk];
-        if (slot < a) {  // an older token: requantised when the page's scale grew
-            if (s == s_old) continue;
-            const float ratio = __fdiv_rn(s_old, s);
-            const uint2 w = *dst;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t v = e4m3x2_to_f16x2((uint16_t)((e < 2 ? w.x : w.y) >> (16 * (e & 1))));
-                f[2 * e] = f16_lo(v) * ratio;
-                f[2 * e + 1] = f16_hi(v) * ratio;
-            }
-        } else if (slot < b) {
-            if constexpr (BF16) {
-                const uint32_t w[4] = {raw[u][0].x, raw[u][0].y, raw[u][0].z, raw[u][0].w};
+            for (int v = 0; v < W; ++v) {
+                const uint32_t w[4] = {raw[x][v].x, raw[x][v].y, raw[x][v].z, raw[x][v].w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    f[2 * e] = __uint_as_float(w[e] << 16);
-                    f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-                }
-            } else {
-#pragma unroll
-                for (int v = 0; v < 2; ++v) {
-                    f[4 * v] = __uint_as_float(raw[u][v].x);
-                    f[4 * v + 1] = __uint_as_float(raw[u][v].y);
-                    f[4 * v + 2] = __uint_as_float(raw[u][v].z);
-                    f[4 * v + 3] = __uint_as_float(raw[u][v].w);
+                    const uint32_t lo = BF16 ? (w[e] << 16) & 0x7fffffffu : w[e] & 0x7fffffffu, hi = w[e] & 0x7fff0000u;
+                    if (lo < 0x7f800000u) amax = max(amax, lo);
+                    if (BF16 && hi < 0x7f800000u) amax = max(amax, hi);
                 }
             }
+        amax = __reduce_max_sync(0xffffffffu, amax);
+        if ((tid & 31) == 0) s_max[u & 1][tid >> 5] = amax;
+        __syncthreads();
 #pragma unroll
-            for (int e = 0; e < kChunk; ++e) f[e] = exact ? f[e] * inv : __fdiv_rn(f[e], s);
+        for (int w = 0; w < NT / 32; ++w) amax = max(amax, s_max[u & 1][w]);
+        if (!(s_old >= 0.f) || (__float_as_uint(s_old) & 0x7f800000u) == 0x7f800000u) {
+            if (tid == 0) atomicOr(err, QUP_ERR_SCALE);
         } else {
-            continue;
+            const float s = fmaxf(pow2(scale_exponent(amax)), s_old);
+            // 1 / s is exact for a power of two; a caller's own scale (s_old kept) takes the division
+            const bool exact = (__float_as_uint(s) & 0x7fffffu) == 0 && s < 8.5e37f;  // 2^126
+            const float inv = exact ? pow2(127 - (int)(__float_as_uint(s) >> 23)) : 0.f;
+#pragma unroll
+            for (int x = 0; x < CH; ++x) {
+                const int at = tid + x * NT, slot = at / kChunksPerToken, part = at % kChunksPerToken;
+                uint2* dst = reinterpret_cast<uint2*>(out + (size_t)slot * kHeadDim + part * kChunk);
+                float f[kChunk];
+                if (slot < a) {  // an older token: requantised when the page's scale grew
+                    if (s == s_old) continue;
+                    const float ratio = __fdiv_rn(s_old, s);
+                    const uint2 w = *dst;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t v = e4m3x2_to_f16x2((uint16_t)((e < 2 ? w.x : w.y) >> (16 * (e & 1))));
+                        f[2 * e] = f16_lo(v) * ratio;
+                        f[2 * e + 1] = f16_hi(v) * ratio;
+                    }
+                } else if (slot < b) {
+                    if constexpr (BF16) {
+                        const uint32_t w[4] = {raw[x][0].x, raw[x][0].y, raw[x][0].z, raw[x][0].w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            f[2 * e] = __uint_as_float(w[e] << 16);
+                            f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+                        }
+                    } else {
+#pragma unroll
+                        for (int v = 0; v < W; ++v) {
+                            f[4 * v] = __uint_as_float(raw[x][v].x);
+                            f[4 * v + 1] = __uint_as_float(raw[x][v].y);
+                            f[4 * v + 2] = __uint_as_float(raw[x][v].z);
+                            f[4 * v + 3] = __uint_as_float(raw[x][v].w);
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < kChunk; ++e) f[e] = exact ? f[e] * inv : __fdiv_rn(f[e], s);
+                } else {
+                    continue;
+                }
+                *dst = make_uint2(pack_e4m3_checked(f), pack_e4m3_checked(f + 4));
+            }
+            if (tid == 0 && (a == 0 || s != s_old)) *scale = s;
         }
-        *dst = make_uint2(pack_e4m3_checked(f), pack_e4m3_checked(f + 4));
+#pragma unroll
+        for (int x = 0; x < CH; ++x)
+#pragma unroll
+            for (int v = 0; v < W; ++v) raw[x][v] = next[x][v];
     }
-    if (tid == 0 && (a == 0 || s != s_old)) *scale = s;
 }
 
 template <int T>
 cudaError_t launch_t(const CacheView& c, const void* k_new, const void* v_new, bool bf16, long long k_stride,
-                     long long v_stride, const int32_t* tok_ptr, int N, unsigned* err, cudaStream_t stream) {
+                     long long v_stride, const int32_t* tok_ptr, int N, int sms, unsigned* err, cudaStream_t stream) {
     const long long items = std::min<long long>(N, N / T + 2ll * c.R);
-    const dim3 grid((unsigned)items, (unsigned)c.Hkv, 2);
-    return bf16 ? launch_pdl(cache_append_kernel<T, true>, grid, dim3(kAppendThreads), 0, stream, c, k_new, v_new,
-                             k_stride, v_stride, tok_ptr, N, err)
-                : launch_pdl(cache_append_kernel<T, false>, grid, dim3(kAppendThreads), 0, stream, c, k_new, v_new,
-                             k_stride, v_stride, tok_ptr, N, err);
+    // units of a CTA: one while the grid is small (a token for each of many requests), up to eight where
+    // there are CTAs enough to fill the SMs several times
+    const int all = 2 * c.Hkv;
+    const int units = (int)std::max<long long>(1, std::min<long long>(std::min(8, all), items * all / (16ll * sms)));
+    const dim3 grid((unsigned)items, (unsigned)((all + units - 1) / units)), block(kAppendThreads<T>);
+    return bf16 ? launch_pdl(cache_append_kernel<T, true>, grid, block, 0, stream, c, k_new, v_new, k_stride, v_stride,
+                             tok_ptr, N, units, err)
+                : launch_pdl(cache_append_kernel<T, false>, grid, block, 0, stream, c, k_new, v_new, k_stride, v_stride,
+                             tok_ptr, N, units, err);
 }
 
 }  // namespace
 
 cudaError_t launch_cache_append(const CacheView& c, const void* k_new, const void* v_new, bool bf16,
-                                long long k_stride, long long v_stride, const int32_t* tok_ptr, int N, unsigned* err,
+                                long long k_stride, long long v_stride, const int32_t* tok_ptr, int N, int sms, unsigned* err,
                                 cudaStream_t stream) {
     if (N == 0 || c.R == 0) return cudaSuccess;
     switch (c.T) {
-        case 16: return launch_t<16>(c, k_new, v_new, bf16, k_stride, v_stride, tok_ptr, N, err, stream);
-        case 32: return launch_t<32>(c, k_new, v_new, bf16, k_stride, v_stride, tok_ptr, N, err, stream);
-        case 64: return launch_t<64>(c, k_new, v_new, bf16, k_stride, v_stride, tok_ptr, N, err, stream);
-        default: return launch_t<128>(c, k_new, v_new, bf16, k_stride, v_stride, tok_ptr, N, err, stream);
+        case 16: return launch_t<16>(c, k_new, v_new, bf16, k_stride, v_stride, tok_ptr, N, sms, err, stream);
+        case 32: return launch_t<32>(c, k_new, v_new, bf16, k_stride, v_stride, tok_ptr, N, sms, err, stream);
+        case 64: return launch_t<64>(c, k_new, v_new, bf16, k_stride, v_stride, tok_ptr, N, sms, err, stream);
+        default: return launch_t<128>(c, k_new, v_new, bf16, k_stride, v_stride, tok_ptr, N, sms, err, stream);
     }
 }
 

@@ -13,7 +13,7 @@
 //
 // Layout: a work unit is 64 tokens of one KV head: 8 KB of K and 8 KB of V, streamed by one
 // producer warp with TMA (128-byte swizzle) through a ring of stages.  Each of the four consumer
-// warps takes 16 tokens of every unit with its own running maximum, sum and output (no exchange
+// warps takes 16 tokens of every unit, two units at a time, with its own running maximum, sum and output (no exchange
 // inside the loop), 16 or 32 rows per tile as mma.m16n8k16 operands straight from the bytes: the
 // order of d inside K's fragments and of d over the output columns is free, so every lane reads 16
 // consecutive bytes of a token (conflict-free under the swizzle) and converts two values at a time.
@@ -27,6 +27,7 @@
 // Bound by DRAM: 2 * 128 bytes per token and KV head.
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "cache.h"
 #include "cache_attn.h"
@@ -114,6 +115,28 @@ __device__ __forceinline__ int request_units(const CacheAttnParams& p, int r, in
     return f ? 0 : tiles_of(q.n, p.g, RT) * p.c.Hkv * units_of(q.len);
 }
 
+// Exclusive prefix over the CTA's threads of v (kThreads of them), and the total; `part` holds one entry per
+// warp.
+__device__ __forceinline__ long long cta_prefix(long long v, long long* part, long long* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long run = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += y;
+    }
+    if (lane == 31) part[warp] = run;
+    __syncthreads();
+    long long before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        before += w < warp ? part[w] : 0;
+        all += part[w];
+    }
+    *total = all;
+    return before + run - v;
+}
+
 // Units of one CTA's run: an equal share of all of them.
 __device__ __forceinline__ int units_per_cta(const CacheAttnParams& p, long long all, int grid) {
     return max(p.per_units, (int)((all + grid - 1) / grid));
@@ -186,16 +209,16 @@ struct Smem {
     static constexpr int kStages = MT == 1 ? 6 : 5;
     static constexpr uint32_t ring = 0;
     static constexpr uint32_t out = ring + kStages * 2 * kTile;             // [RT][128] fp32
-    static constexpr uint32_t qfrag = out + RT * kHeadDim * 4;              // MT > 1: [MT][8][32] uint4
-    static constexpr uint32_t meta = qfrag + (MT > 1 ? RT * kHeadDim * 2 : 0);  // [kStages][kMaxBoxes]
+    static constexpr uint32_t qfrag = out + RT * kHeadDim * 4;  // [MT][8][32] uint4
+    static constexpr uint32_t meta = qfrag + RT * kHeadDim * 2;  // [kStages][kMaxBoxes]
     static constexpr uint32_t ml = meta + kStages * kMaxBoxes * sizeof(PageMeta);  // [kConsumers][RT] float2
     static constexpr uint32_t bars = ml + kConsumers * RT * 8;
     static constexpr uint32_t misc = bars + 2 * kStages * 8;  // abort flag, start, scan
-    static constexpr uint32_t list = misc + 64 + 8 * kThreads;  // TopK: bitmap, prefix, pages, masks
+    static constexpr uint32_t list = misc + 64 + 64;  // TopK: bitmap, prefix, pages, masks
 };
 
 template <int MT, bool SPARSE, bool WEIGHTS>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, MT == 1 ? 2 : 1)
     cache_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const __grid_constant__ CacheAttnParams p) {
     using L = Smem<MT>;
@@ -240,13 +263,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         unsigned bad = 0;
         for (int r = sp.r0; r < sp.r1; ++r) sum += request_units(p, r, RT, &bad);
         if (bad) atomicOr(p.err, bad);
-        scan[tid] = sum;
-        __syncthreads();
-        long long mine = 0, all = 0;
-        for (int t = 0; t < kThreads; ++t) {
-            mine += t < tid ? scan[t] : 0;
-            all += scan[t];
-        }
+        long long all = 0;
+        const long long mine = cta_prefix(sum, scan, &all);
         const int per = units_per_cta(p, all, (int)gridDim.x);
         const long long u0 = (long long)blockIdx.x * per;
         if (u0 < all) {
@@ -306,13 +324,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                 before[w] = sum;
                 sum += __popc(bits[w]);
             }
-            scan[tid] = sum;
-            __syncthreads();
-            int mine = 0, all = 0;
-            for (int t = 0; t < kThreads; ++t) {
-                mine += t < tid ? (int)scan[t] : 0;
-                all += (int)scan[t];
-            }
+            long long total = 0;
+            const int mine = (int)cta_prefix(sum, scan, &total), all = (int)total;
             for (int w = w0; w < w1; ++w) before[w] += mine;
             const int share = (all + p.nsplit - 1) / p.nsplit;
             list_lo = min(all, split * share);
@@ -453,11 +466,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int row0 = SPARSE ? 0 : sg.tile * RT;                     // in (query, head) order
         const int e0 = sg.b0, e1 = min(sg.b1, sg.nvis);
         // ---- Q fragments: lane (i, q4) holds d = 32 q4 + 4 ks .. + 3 of rows i and i + 8
-        uint32_t qa[MT == 1 ? 8 : 1][4];
         float rs[MT][2];
         int vis[MT][2];  // tokens each row sees
         float m[MT][2], l[MT][2], o[MT][16][4];
-        if (MT > 1) bar_sync(1, 32 * kConsumers);  // the last segment's fragments are done with
+        bar_sync(1, 32 * kConsumers);  // the last segment's fragments are done with
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             uint32_t f[8][4];
@@ -496,12 +508,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 m[mt][hf] = kNegInf;
                 l[mt][hf] = 0.f;
             }
-            if constexpr (MT == 1) {
-#pragma unroll
-                for (int s = 0; s < 8; ++s)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) qa[s][e] = f[s][e];
-            } else if (warp == mt) {
+            if (warp == mt) {
 #pragma unroll
                 for (int s = 0; s < 8; ++s)
                     s_q[(mt * 8 + s) * 32 + lane] = make_uint4(f[s][0], f[s][1], f[s][2], f[s][3]);
@@ -511,68 +518,99 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[mt][j][e] = 0.f;
         }
-        if (MT > 1) bar_sync(1, 32 * kConsumers);
+        bar_sync(1, 32 * kConsumers);
         // tokens that every row of the tile sees, and that any row sees
         const int vis_all = SPARSE ? sg.len : sg.len - sg.n + row0 / g + 1;
         const int vis_any = SPARSE ? sg.len : sg.len - sg.n + (row0 + rows - 1) / g + 1;
         const uint32_t all_rows = SPARSE ? (rows == 32 ? 0xffffffffu : (1u << rows) - 1u) : 0xffffffffu;
 
-        for (int b = e0; b < e1; ++b, ++it) {
-            const uint32_t slot = it % NS, par = (it / NS) & 1;
-            if (!dead && !mbar_wait(full0 + 8 * slot, par, abort_flag, p.err, QUP_ERR_TIMEOUT, p.wait_limit_ns))
-                dead = true;
-            if (dead) continue;
-            const PageMeta pm = meta[slot * kMaxBoxes + 16 * warp / box];
-            const int pos = pm.pos + (16 * warp) % box;  // of the warp's first token
-            if (pm.mask != 0u && pos < vis_any) {
-                const uint32_t kt = sbase + L::ring + slot * 2 * kTile, vt = kt + kTile;
-                // ---- S = Q K^T: token 8 nt + i of the warp, d = 32 q4 .. + 31 of it in two loads
-                float c[MT][2][4];
+        // page weights: this tile's rows, mass_rows apart for every 16 tokens
+        const size_t mass_rows = (size_t)p.max_q * g;
+        float2* const mass = !WEIGHTS ? nullptr
+                                      : p.ws_mass + ((size_t)sg.p0 * p.c.Hkv + (size_t)sg.h * sg.np) * (T / 16) * mass_rows +
+                                            (SPARSE ? (sg.q0 - p.q_ptr[sg.r]) * g : row0);
+        // One turn: NG units, 16 tokens of each.  Two at a time hide each other's latencies (products in a
+        // chain, conversions, the row maximum's shuffles): one warp alone keeps its scheduler a third busy.
+        const auto turn = [&](auto groups) {
+            constexpr int NG = decltype(groups)::value;
+            PageMeta pm[NG];
+            int pos[NG];  // of the warp's first token of each
+            bool live[NG], mixed[NG], any = false;
+            uint32_t tile[NG];
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
+            for (int n = 0; n < NG; ++n) {
+                const uint32_t slot = (it + n) % NS, par = ((it + n) / NS) & 1;
+                if (!dead && !mbar_wait(full0 + 8 * slot, par, abort_flag, p.err, QUP_ERR_TIMEOUT, p.wait_limit_ns))
+                    dead = true;
+                pm[n] = meta[slot * kMaxBoxes + 16 * warp / box];
+                pos[n] = pm[n].pos + (16 * warp) % box;
+                live[n] = pm[n].mask != 0u && pos[n] < vis_any;
+                mixed[n] = !live[n] || pos[n] + 16 > vis_all || (pm[n].mask & all_rows) != all_rows;
+                any = any || live[n];
+                tile[n] = sbase + L::ring + slot * 2 * kTile;
+            }
+            if (dead) return;
+            if (any) {
+                // ---- S = Q K^T: token 8 nt + i of the warp, d = 32 q4 .. + 31 of it in two loads
+                float c[NG][MT][2][4];
+#pragma unroll
+                for (int n = 0; n < NG; ++n)
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) c[mt][nt][e] = 0.f;
-                    const uint32_t row = kt + (16 * warp + 8 * nt + i) * kHeadDim;
+                        for (int e = 0; e < 8; ++e) c[n][mt][e >> 2][e & 3] = 0.f;
 #pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        const uint4 k = lds128(row + (((2 * q4 + s) ^ i) << 4));
-                        const uint32_t w[4] = {k.x, k.y, k.z, k.w};
+                for (int s = 0; s < 2; ++s) {
+                    uint4 k[NG][2];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint32_t b0 = cvt_e4m3x2(w[e]), b1 = cvt_e4m3x2(w[e] >> 16);
-                            if constexpr (MT == 1) {
-                                mma16816(c[0][nt], qa[4 * s + e], b0, b1);
-                            } else {
+                    for (int n = 0; n < NG; ++n)
 #pragma unroll
-                                for (int mt = 0; mt < MT; ++mt) {
-                                    const uint4 a = s_q[(mt * 8 + 4 * s + e) * 32 + lane];
-                                    const uint32_t aw[4] = {a.x, a.y, a.z, a.w};
-                                    mma16816(c[mt][nt], aw, b0, b1);
-                                }
-                            }
+                        for (int nt = 0; nt < 2; ++nt)
+                            k[n][nt] = lds128(tile[n] + (16 * warp + 8 * nt + i) * kHeadDim + (((2 * q4 + s) ^ i) << 4));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t aw[MT][4];
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) {
+                            const uint4 a = s_q[(mt * 8 + 4 * s + e) * 32 + lane];
+                            aw[mt][0] = a.x;
+                            aw[mt][1] = a.y;
+                            aw[mt][2] = a.z;
+                            aw[mt][3] = a.w;
                         }
+#pragma unroll
+                        for (int n = 0; n < NG; ++n)
+#pragma unroll
+                            for (int nt = 0; nt < 2; ++nt) {
+                                const uint32_t w = e < 2 ? (e == 0 ? k[n][nt].x : k[n][nt].y)
+                                                         : (e == 2 ? k[n][nt].z : k[n][nt].w);
+                                const uint32_t b0 = cvt_e4m3x2(w), b1 = cvt_e4m3x2(w >> 16);
+#pragma unroll
+                                for (int mt = 0; mt < MT; ++mt) mma16816(c[n][mt][nt], aw[mt], b0, b1);
+                            }
                     }
                 }
-                const bool mixed = pos + 16 > vis_all || (pm.mask & all_rows) != all_rows;
-                uint32_t pa[MT][4];
+                uint32_t pa[NG][MT][4];
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf) {
-                        const float f = rs[mt][hf] * pm.ks;
-                        float x[4];
+                        const int rr = 16 * mt + 8 * hf + i;
+                        float x[NG][4], bm = kNegInf;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) x[e] = fmaf(c[mt][e >> 1][2 * hf + (e & 1)], f, pm.vs_log2);
-                        if (mixed) {
-                            const int rr = 16 * mt + 8 * hf + i;
-                            const bool on = !SPARSE || ((pm.mask >> (rr & 31)) & 1u);
+                        for (int n = 0; n < NG; ++n) {
+                            const float f = rs[mt][hf] * pm[n].ks;
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
-                                if (!on || pos + 8 * (e >> 1) + 2 * q4 + (e & 1) >= vis[mt][hf]) x[e] = kNegInf;
+                                x[n][e] = fmaf(c[n][mt][e >> 1][2 * hf + (e & 1)], f, pm[n].vs_log2);
+                            if (mixed[n]) {
+                                const bool on = live[n] && (!SPARSE || ((pm[n].mask >> (rr & 31)) & 1u));
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (!on || pos[n] + 8 * (e >> 1) + 2 * q4 + (e & 1) >= vis[mt][hf]) x[n][e] = kNegInf;
+                            }
+                            bm = fmaxf(bm, fmaxf(fmaxf(x[n][0], x[n][1]), fmaxf(x[n][2], x[n][3])));
                         }
-                        float bm = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
                         bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 1));
                         bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 2));
                         if (__any_sync(0xffffffffu, bm > m[mt][hf] + kLazy)) {
@@ -588,111 +626,118 @@ __global__ void __launch_bounds__(kThreads, 2)
                         }
                         const float sub = m[mt][hf] == kNegInf ? 0.f : m[mt][hf] - kOffset;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) x[e] = ex2(x[e] - sub);
-                        float sum = ((x[0] + x[1]) + (x[2] + x[3])) * pm.vs_inv;
-                        l[mt][hf] += sum;
-                        if constexpr (WEIGHTS) {
-                            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                            const int rr = 16 * mt + 8 * hf + i;
-                            if (q4 == 0 && rr < rows) {
-                                const size_t rowsw = (size_t)p.max_q * g;
-                                const size_t at = ((size_t)sg.p0 * p.c.Hkv + (size_t)sg.h * sg.np) * (T / 16) * rowsw +
-                                                  (size_t)(pos / 16) * rowsw +
-                                                  (SPARSE ? (sg.q0 - p.q_ptr[sg.r]) * g : row0) + rr;
-                                p.ws_mass[at] = make_float2(sum, m[mt][hf]);
+                        for (int n = 0; n < NG; ++n) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) x[n][e] = ex2(x[n][e] - sub);
+                            float sum = ((x[n][0] + x[n][1]) + (x[n][2] + x[n][3])) * pm[n].vs_inv;
+                            l[mt][hf] += sum;
+                            if constexpr (WEIGHTS) {
+                                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                                if (q4 == 0 && rr < rows && pos[n] < vis_any)
+                                    mass[(size_t)(pos[n] / 16) * mass_rows + rr] = make_float2(sum, m[mt][hf]);
                             }
+                            pa[n][mt][hf] = pack_f16x2(x[n][0], x[n][1]);
+                            pa[n][mt][hf + 2] = pack_f16x2(x[n][2], x[n][3]);
                         }
-                        pa[mt][hf] = pack_f16x2(x[0], x[1]);
-                        pa[mt][hf + 2] = pack_f16x2(x[2], x[3]);
                     }
                 }
                 // ---- O += P V: tokens 2 q4, + 1, + 8, + 9 of the warp, d = 16 i .. + 15 of each
-                uint32_t v[4][4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int t = 2 * q4 + (e & 1) + 8 * (e >> 1);
-                    const uint4 w = lds128(vt + (16 * warp + t) * kHeadDim + ((i ^ (t & 7)) << 4));
-                    v[e][0] = w.x;
-                    v[e][1] = w.y;
-                    v[e][2] = w.z;
-                    v[e][3] = w.w;
-                }
-                bool slow = false;
-                if (mixed) {
-                    // bytes behind the last visible token may be anything; a NaN that some rows see and
-                    // others do not must not reach the others as 0 * NaN
-                    bool nan = false;
+                for (int n = 0; n < NG; ++n) {
+                    uint32_t v[4][4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        if (pos + 2 * q4 + (e & 1) + 8 * (e >> 1) >= vis_any) v[e][0] = v[e][1] = v[e][2] = v[e][3] = 0u;
-                        nan = nan || has_nan_byte(v[e][0]) || has_nan_byte(v[e][1]) || has_nan_byte(v[e][2]) ||
-                              has_nan_byte(v[e][3]);
+                        const int t = 2 * q4 + (e & 1) + 8 * (e >> 1);
+                        const uint4 w = lds128(tile[n] + kTile + (16 * warp + t) * kHeadDim + ((i ^ (t & 7)) << 4));
+                        v[e][0] = w.x;
+                        v[e][1] = w.y;
+                        v[e][2] = w.z;
+                        v[e][3] = w.w;
                     }
-                    slow = __any_sync(0xffffffffu, nan);
-                }
-                if (!slow) {
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-#pragma unroll
-                        for (int hi = 0; hi < 2; ++hi) {
-                            const uint32_t x0 = __byte_perm(v[0][w], v[1][w], hi ? 0x7362 : 0x5140);
-                            const uint32_t x1 = __byte_perm(v[2][w], v[3][w], hi ? 0x7362 : 0x5140);
-#pragma unroll
-                            for (int d = 0; d < 2; ++d) {
-                                const uint32_t b0 = cvt_e4m3x2(d ? x0 >> 16 : x0), b1 = cvt_e4m3x2(d ? x1 >> 16 : x1);
-#pragma unroll
-                                for (int mt = 0; mt < MT; ++mt) mma16816(o[mt][4 * w + 2 * hi + d], pa[mt], b0, b1);
-                            }
-                        }
-                    }
-                } else {
-                    // row by row: the other rows' weights and the tokens the row does not see are zero
-                    for (int rr = 0; rr < rows; ++rr) {
-                        const int rv = SPARSE ? sg.len : sg.len - sg.n + (row0 + rr) / g + 1;
-                        const bool on = !SPARSE || ((pm.mask >> rr) & 1u);
-                        const int mine_mt = rr >> 4, mine_hf = (rr >> 3) & 1;
-                        const bool own = (rr & 7) == i;
-                        uint32_t a[4];
+                    bool slow = false;
+                    if (mixed[n]) {
+                        // bytes behind the last visible token may be anything; a NaN that some rows see and
+                        // others do not must not reach the others as 0 * NaN
+                        bool nan = false;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            uint32_t x = pa[0][e];
-                            if (MT > 1 && mine_mt == 1) x = pa[MT - 1][e];
-                            a[e] = own && (e & 1) == mine_hf ? x : 0u;
+                            if (!live[n] || pos[n] + 2 * q4 + (e & 1) + 8 * (e >> 1) >= vis_any)
+                                v[e][0] = v[e][1] = v[e][2] = v[e][3] = 0u;
+                            nan = nan || has_nan_byte(v[e][0]) || has_nan_byte(v[e][1]) || has_nan_byte(v[e][2]) ||
+                                  has_nan_byte(v[e][3]);
                         }
+                        slow = __any_sync(0xffffffffu, nan);
+                    }
+                    if (!slow) {
 #pragma unroll
                         for (int w = 0; w < 4; ++w) {
-                            uint32_t z[4];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                z[e] = on && pos + 2 * q4 + (e & 1) + 8 * (e >> 1) < rv ? v[e][w] : 0u;
+                            for (int hi = 0; hi < 2; ++hi) {
+                                const uint32_t x0 = __byte_perm(v[0][w], v[1][w], hi ? 0x7362 : 0x5140);
+                                const uint32_t x1 = __byte_perm(v[2][w], v[3][w], hi ? 0x7362 : 0x5140);
 #pragma unroll
-                            for (int d = 0; d < 4; ++d) {
-                                const uint32_t x0 = __byte_perm(z[0], z[1], d < 2 ? 0x5140 : 0x7362);
-                                const uint32_t x1 = __byte_perm(z[2], z[3], d < 2 ? 0x5140 : 0x7362);
-                                float t[4] = {0.f, 0.f, 0.f, 0.f};
-                                mma16816(t, a, cvt_e4m3x2(d & 1 ? x0 >> 16 : x0), cvt_e4m3x2(d & 1 ? x1 >> 16 : x1));
+                                for (int d = 0; d < 2; ++d) {
+                                    const uint32_t b0 = cvt_e4m3x2(d ? x0 >> 16 : x0), b1 = cvt_e4m3x2(d ? x1 >> 16 : x1);
 #pragma unroll
-                                for (int mt = 0; mt < MT; ++mt)
+                                    for (int mt = 0; mt < MT; ++mt) mma16816(o[mt][4 * w + 2 * hi + d], pa[n][mt], b0, b1);
+                                }
+                            }
+                        }
+                    } else {
+                        // row by row: the other rows' weights and the tokens the row does not see are zero
+#pragma unroll 1
+                        for (int rr = 0; rr < rows; ++rr) {
+                            const int rv = SPARSE ? sg.len : sg.len - sg.n + (row0 + rr) / g + 1;
+                            const bool on = !SPARSE || ((pm[n].mask >> rr) & 1u);
+                            const int mine_mt = rr >> 4, mine_hf = (rr >> 3) & 1;
+                            const bool own = (rr & 7) == i;
+                            uint32_t a[4];
 #pragma unroll
-                                    for (int e = 0; e < 4; ++e)
-                                        if (own && mt == mine_mt && (e >> 1) == mine_hf) o[mt][4 * w + d][e] += t[e];
+                            for (int e = 0; e < 4; ++e) {
+                                uint32_t x = pa[n][0][e];
+                                if (MT > 1 && mine_mt == 1) x = pa[n][MT - 1][e];
+                                a[e] = own && (e & 1) == mine_hf ? x : 0u;
+                            }
+#pragma unroll
+                            for (int w = 0; w < 4; ++w) {
+                                uint32_t z[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    z[e] = on && pos[n] + 2 * q4 + (e & 1) + 8 * (e >> 1) < rv ? v[e][w] : 0u;
+#pragma unroll
+                                for (int d = 0; d < 4; ++d) {
+                                    const uint32_t x0 = __byte_perm(z[0], z[1], d < 2 ? 0x5140 : 0x7362);
+                                    const uint32_t x1 = __byte_perm(z[2], z[3], d < 2 ? 0x5140 : 0x7362);
+                                    float t[4] = {0.f, 0.f, 0.f, 0.f};
+                                    mma16816(t, a, cvt_e4m3x2(d & 1 ? x0 >> 16 : x0), cvt_e4m3x2(d & 1 ? x1 >> 16 : x1));
+#pragma unroll
+                                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                                        for (int e = 0; e < 4; ++e)
+                                            if (own && mt == mine_mt && (e >> 1) == mine_hf) o[mt][4 * w + d][e] += t[e];
+                                }
                             }
                         }
                     }
                 }
             } else if (WEIGHTS) {
-                // a page that no row reads (a bad page): zero mass
-                for (int rr = lane; rr < rows && pos < vis_any; rr += 32) {
-                    const size_t rowsw = (size_t)p.max_q * g;
-                    p.ws_mass[((size_t)sg.p0 * p.c.Hkv + (size_t)sg.h * sg.np) * (T / 16) * rowsw +
-                              (size_t)(pos / 16) * rowsw + (SPARSE ? (sg.q0 - p.q_ptr[sg.r]) * g : row0) + rr] =
-                        make_float2(0.f, 0.f);
-                }
+                // pages that no row reads (bad pages): zero mass
+#pragma unroll
+                for (int n = 0; n < NG; ++n)
+                    for (int rr = lane; rr < rows && pos[n] < vis_any; rr += 32)
+                        mass[(size_t)(pos[n] / 16) * mass_rows + rr] = make_float2(0.f, 0.f);
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(empty0 + 8 * slot);
-        }
+            if (lane == 0)
+#pragma unroll
+                for (int n = 0; n < NG; ++n) mbar_arrive(empty0 + 8 * ((it + n) % NS));
+            it += NG;
+        };
+        int b = e0;
+        if (MT == 1)
+            for (; b + 1 < e1 && !dead; b += 2) turn(std::integral_constant<int, 2>());
+        for (; b < e1 && !dead; ++b) turn(std::integral_constant<int, 1>());
 
         // ---- the four warps' results, joined
 #pragma unroll
@@ -899,50 +944,64 @@ __global__ void __launch_bounds__(kHeadDim) cache_merge_kernel(const __grid_cons
 // ------------------------------------------------------------------ page weights
 // weight[page][h] = sum over the request's rows of the softmax weight on the page's tokens, from the
 // sums that the attention kernel kept for every 16 tokens and row (and the maximum each was
-// relative to).  One warp per (page, KV head); lanes over (16 tokens, row), added in a fixed order.
-constexpr int kWeightWarps = 8;
+// relative to).  One warp per KV head and a few pages, 32 / S pages at a time with S lanes on each; added
+// in a fixed order.  Bound by the latency of its dependent loads.
+constexpr int kWeightWarps = 8, kWeightTurns = 2;
 template <bool SPARSE>
-__global__ void __launch_bounds__(32 * kWeightWarps) cache_weight_kernel(const __grid_constant__ CacheAttnParams p) {
+__global__ void __launch_bounds__(32 * kWeightWarps) cache_weight_kernel(const __grid_constant__ CacheAttnParams p,
+                                                                         int S) {
     grid_dep_wait();
     const int lane = threadIdx.x & 31;
     const long long x = (long long)blockIdx.x * kWeightWarps + (threadIdx.x >> 5);
-    if (x >= (long long)p.c.total_pages * p.c.Hkv) return;
-    const int u = (int)(x / p.c.Hkv), h = (int)(x - (long long)u * p.c.Hkv);
-    int r = -1;
-    for (int y0 = 0; y0 < p.c.R && r < 0; y0 += 32) {
-        const int y = y0 + lane;
-        const bool in = y < p.c.R && p.c.page_ptr[y] <= u && u < p.c.page_ptr[y + 1];
-        const unsigned bal = __ballot_sync(0xffffffffu, in);
-        if (bal) r = y0 + __ffs(bal) - 1;
-    }
-    if (r < 0) return;  // a page of no request: left as it is
-    const Request q = load_request(p.q_ptr, p.Nq, p.c.kv_len, p.c.page_ptr, p.c.total_pages, p.c.T, r);
-    float sum = 0.f;
-    const int T = p.c.T, g = p.g, pg = u - q.p0;
-    if (request_fault(p, q) == 0u) {
-        const size_t rowsw = (size_t)p.max_q * g;
-        const float2* src = p.ws_mass + ((size_t)q.p0 * p.c.Hkv + (size_t)h * q.np) * (T / 16) * rowsw +
-                            (size_t)pg * (T / 16) * rowsw;
-        // the chunk kernel keeps one sum for each page and row, in the place of its first 16 tokens
-        const int rows = q.n * g, total = rows * (!SPARSE && rows >= p.big_rows ? 1 : T / 16);
-        const uint32_t* bits = SPARSE ? p.ws_bits + (size_t)(q.p0 / 32 + r) * p.max_q * p.c.Hkv : nullptr;
-        for (int e = lane; e < total; e += 32) {
-            const int grp = e / rows, row = e - grp * rows, qi = row / g, j = row - qi * g;
-            const int pos = pg * T + 16 * grp;
-            // the attention kernel reads whole tiles: what a row does not see it has as zero, but
-            // 16 tokens that no row of its tile sees it leaves out
-            if (pos >= q.len - q.n + qi + 1) continue;
-            if (SPARSE && !((bits[((size_t)qi * p.c.Hkv + h) * ((q.np + 31) / 32) + (pg >> 5)] >> (pg & 31)) & 1u))
-                continue;
-            const float2 a = src[(size_t)grp * rowsw + row];
-            const float l2 = p.ws_lse[(size_t)(q.q0 + qi) * p.Hq + h * g + j];
-            // a row whose running maximum was still -inf has 0 here; NaN stays NaN
-            sum += a.x == 0.f ? 0.f : a.x * ex2((a.y == kNegInf ? 0.f : a.y - kOffset) - l2);
+    const int run = (int)(x / p.c.Hkv), h = (int)(x - (long long)run * p.c.Hkv);
+    const int u0 = run * kWeightTurns * (32 / S), u1 = min(p.c.total_pages, u0 + kWeightTurns * (32 / S));
+    if (u0 >= p.c.total_pages) return;
+    const int T = p.c.T, g = p.g, sub = lane & (S - 1);
+    const size_t rowsw = (size_t)p.max_q * g;
+    // the lane's page and its request, looked up again only past the request's end
+    int r = -1, end = -1;
+    Request q{};
+    bool ok = false;
+    for (int u = u0 + lane / S; u - lane / S < u1; u += 32 / S) {
+        if (u < u1 && u >= end) {
+            int lo = 0, hi = p.c.R;  // the last request that begins at or before the page
+            while (lo + 1 < hi) {
+                const int mid = (lo + hi) / 2;
+                if (p.c.page_ptr[mid] <= u) lo = mid;
+                else hi = mid;
+            }
+            r = p.c.page_ptr[lo] <= u && u < p.c.page_ptr[lo + 1] ? lo : -1;
+            if (r >= 0) {
+                q = load_request(p.q_ptr, p.Nq, p.c.kv_len, p.c.page_ptr, p.c.total_pages, T, r);
+                ok = request_fault(p, q) == 0u;
+                end = p.c.page_ptr[r + 1];
+            }
         }
-#pragma unroll
-        for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+        const bool on = u < u1 && r >= 0;  // a page of no request is left as it is
+        float sum = 0.f;
+        if (on && ok) {
+            const int pg = u - q.p0;
+            const float2* src = p.ws_mass + ((size_t)q.p0 * p.c.Hkv + (size_t)h * q.np + pg) * (T / 16) * rowsw;
+            // the chunk kernel keeps one sum for each page and row, in the place of its first 16 tokens
+            const int rows = q.n * g, total = rows * (!SPARSE && rows >= p.big_rows ? 1 : T / 16);
+            const uint32_t* bits = SPARSE ? p.ws_bits + (size_t)(q.p0 / 32 + r) * p.max_q * p.c.Hkv : nullptr;
+            for (int e = pg * T < q.len ? sub : total; e < total; e += S) {
+                const int grp = e / rows, row = e - grp * rows, qi = row / g, j = row - qi * g;
+                const int pos = pg * T + 16 * grp;
+                // the attention kernel reads whole tiles: what a row does not see it has as zero, but
+                // 16 tokens that no row of its tile sees it leaves out
+                if (pos >= q.len - q.n + qi + 1) continue;
+                if (SPARSE && !((bits[((size_t)qi * p.c.Hkv + h) * ((q.np + 31) / 32) + (pg >> 5)] >> (pg & 31)) & 1u))
+                    continue;
+                const float2 a = src[(size_t)grp * rowsw + row];
+                const float l2 = p.ws_lse[(size_t)(q.q0 + qi) * p.Hq + h * g + j];
+                // a row whose running maximum was still -inf has 0 here; NaN stays NaN
+                sum += a.x == 0.f ? 0.f : a.x * ex2((a.y == kNegInf ? 0.f : a.y - kOffset) - l2);
+            }
+        }
+        for (int s = S / 2; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+        if (on && sub == 0) p.weight[(size_t)u * p.c.Hkv + h] = sum;
     }
-    if (lane == 0) p.weight[(size_t)u * p.c.Hkv + h] = sum;
 }
 
 template <int MT, bool SPARSE, bool WEIGHTS>
@@ -954,22 +1013,22 @@ cudaError_t launch_main(const CUtensorMap& tmK, const CUtensorMap& tmV, const Ca
     return launch_pdl(cache_attn_kernel<MT, SPARSE, WEIGHTS>, dim3(grid), dim3(kThreads), smem, stream, tmK, tmV, p);
 }
 
+// TopK pages: 16 or 32 rows (the heads of a KV head); all pages: 16 rows, more are the chunk kernel's.
 template <int MT>
-cudaError_t launch_mt(const CUtensorMap& tmK, const CUtensorMap& tmV, const CacheAttnParams& p, int grid, int items,
-                      cudaStream_t stream) {
-    const bool sparse = p.topk != nullptr, weights = p.weight != nullptr;
-    cudaError_t e;
-    if (sparse)
-        e = weights ? launch_main<MT, true, true>(tmK, tmV, p, grid, stream)
-                    : launch_main<MT, true, false>(tmK, tmV, p, grid, stream);
-    else
-        e = weights ? launch_main<MT, false, true>(tmK, tmV, p, grid, stream)
-                    : launch_main<MT, false, false>(tmK, tmV, p, grid, stream);
+cudaError_t launch_sparse(const CUtensorMap& tmK, const CUtensorMap& tmV, const CacheAttnParams& p, int grid, int items,
+                          cudaStream_t stream) {
+    const cudaError_t e = p.weight ? launch_main<MT, true, true>(tmK, tmV, p, grid, stream)
+                                   : launch_main<MT, true, false>(tmK, tmV, p, grid, stream);
+    if (e != cudaSuccess || p.nsplit == 1) return e;
+    return launch_pdl(cache_merge_kernel<16 * MT, true>, dim3(items), dim3(kHeadDim), 0, stream, p, grid);
+}
+
+cudaError_t launch_dense(const CUtensorMap& tmK, const CUtensorMap& tmV, const CacheAttnParams& p, int grid, int items,
+                         cudaStream_t stream) {
+    const cudaError_t e = p.weight ? launch_main<1, false, true>(tmK, tmV, p, grid, stream)
+                                   : launch_main<1, false, false>(tmK, tmV, p, grid, stream);
     if (e != cudaSuccess) return e;
-    if (!sparse) e = launch_pdl(cache_merge_kernel<16 * MT, false>, dim3(items), dim3(kHeadDim), 0, stream, p, grid);
-    else if (p.nsplit > 1)
-        e = launch_pdl(cache_merge_kernel<16 * MT, true>, dim3(items), dim3(kHeadDim), 0, stream, p, grid);
-    return e;
+    return launch_pdl(cache_merge_kernel<16, false>, dim3(items), dim3(kHeadDim), 0, stream, p, grid);
 }
 
 }  // namespace
@@ -982,14 +1041,20 @@ size_t cache_attn_smem(int mt, bool sparse, int max_pages, int list_cap) {
 
 cudaError_t launch_cache_attn(int mt, const CUtensorMap& tmK, const CUtensorMap& tmV, const CacheAttnParams& p,
                               int grid, int items, cudaStream_t stream) {
-    return mt == 1 ? launch_mt<1>(tmK, tmV, p, grid, items, stream) : launch_mt<2>(tmK, tmV, p, grid, items, stream);
+    if (!p.topk) return launch_dense(tmK, tmV, p, grid, items, stream);
+    return mt == 1 ? launch_sparse<1>(tmK, tmV, p, grid, items, stream) : launch_sparse<2>(tmK, tmV, p, grid, items, stream);
 }
 
 cudaError_t launch_cache_weights(const CacheAttnParams& p, cudaStream_t stream) {
-    const long long warps = (long long)p.c.total_pages * p.c.Hkv;
+    // lanes on a page: as many as it has sums, up to a warp
+    const long long sums = (long long)p.max_q * p.g * (p.max_q * p.g >= p.big_rows ? 1 : p.c.T / 16);
+    int S = 2;
+    while (S < 32 && S < sums) S *= 2;
+    const int pages = kWeightTurns * (32 / S);
+    const long long warps = (long long)((p.c.total_pages + pages - 1) / pages) * p.c.Hkv;
     const dim3 grid((unsigned)((warps + kWeightWarps - 1) / kWeightWarps));
-    return p.topk ? launch_pdl(cache_weight_kernel<true>, grid, dim3(32 * kWeightWarps), 0, stream, p)
-                  : launch_pdl(cache_weight_kernel<false>, grid, dim3(32 * kWeightWarps), 0, stream, p);
+    return p.topk ? launch_pdl(cache_weight_kernel<true>, grid, dim3(32 * kWeightWarps), 0, stream, p, S)
+                  : launch_pdl(cache_weight_kernel<false>, grid, dim3(32 * kWeightWarps), 0, stream, p, S);
 }
 
 }  // namespace qup

@@ -77,8 +77,8 @@ struct Layout {
     static constexpr uint32_t meta = v16 + 4 * kTile;
     static constexpr uint32_t nan = meta + kNM * sizeof(StepMeta);  // [kMarks]
     static constexpr uint32_t bars = nan + kMarks * sizeof(NanMarks);
-    static constexpr uint32_t scan = bars + 8 * 40;                 // [kThreads] int64
-    static constexpr uint32_t misc = scan + 8 * kThreads;
+    static constexpr uint32_t scan = bars + 8 * 40;                 // one int64 per warp
+    static constexpr uint32_t misc = scan + 8 * 16;
     static constexpr uint32_t walks = misc + 64;                    // one per warp
     static constexpr uint32_t total = walks + (kThreads / 32) * 128;
 };
@@ -327,12 +327,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             sum += it.total(p);
         }
         if (fault) atomicOr(p.err, fault);
-        scan[tid] = sum;
+        long long run = sum;  // prefix over the CTA
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, run, o);
+            if (lane >= o) run += y;
+        }
+        if (lane == 31) scan[warp] = run;
         __syncthreads();
-        long long mine = 0, all = 0;
-        const int used = min(kThreads, p.c.R);  // threads past the last request have no steps
-        for (int t = 0; t < used; ++t) {
-            mine += t < tid ? scan[t] : 0;
+        long long mine = run - sum, all = 0;
+#pragma unroll
+        for (int t = 0; t < kThreads / 32; ++t) {
+            mine += t < warp ? scan[t] : 0;
             all += scan[t];
         }
         const long long per = max((all + gridDim.x - 1) / gridDim.x, 1ll);
@@ -951,9 +957,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------ join of cut items
-// CTA (c, y): if the last item of run c begins there and goes on, its rows [32 y, 32 y + 32): the parts
+// CTA (c, y): if the last item of run c begins there and goes on, its rows [8 y, 8 y + 8): the parts
 // of runs c, c + 1, ... in order, up to the run in which the item ends.
-constexpr int kJoinRows = 32;
+constexpr int kJoinRows = 8;
 __global__ void __launch_bounds__(kHeadDim) cache_chunk_join_kernel(const __grid_constant__ CacheAttnParams p, int runs) {
     grid_dep_wait();
     const ChunkSpan a = p.spans[blockIdx.x];
