@@ -54,10 +54,10 @@ struct AttnWs {
 };
 
 // The partial results of an all-pages call: two of each CTA.  Those of a TopK call: one of each CTA
-// of a (query, KV head), which is cut only while all of them are at most kCacheMaxCtas.
+// of a (query, KV head), which is cut only while all of them fit the SMs at once.
 AttnWs attn_ws_layout(const qup_cache* c, int Nq, int max_q, int Hq, bool weights) {
     AttnWs w;
-    const size_t parts = 2 * (size_t)qup::kCacheMaxCtas * qup::kCacheMaxRows;
+    const size_t parts = qup::kCachePartRows;
     size_t off = 0;
     w.part_o = off;
     off = align256(off + parts * qup::kHeadDim * sizeof(float));
@@ -154,11 +154,12 @@ int qup_cache_attn(const qup_cache* cache, const void* Q, int64_t q_stride, cons
     const int64_t big = (int64_t)max_q * g;
     const bool chunk = !sparse && big > qup::kCacheSmallRows;
     const bool small = !chunk || (int64_t)c.R * max_q != Nq;
-    const int mt = sparse && g > 16 ? 2 : 1, rt = 16 * mt;
+    const int64_t small_rows = sparse ? g : std::min<int64_t>(big, qup::kCacheSmallRows);
+    const int nt = small_rows <= 8 ? 1 : (small_rows <= 16 ? 2 : 4), rt = 8 * nt;
     qup::CacheAttnParams p;
     std::memset(&p, 0, sizeof(p));
     p.big_rows = !chunk ? 0x7fffffff : (small ? qup::kCacheSmallRows + 1 : 1);
-    p.max_tiles = (int)((std::min<int64_t>(big, chunk ? qup::kCacheSmallRows : big) + rt - 1) / rt);
+    p.max_tiles = (int)((small_rows + rt - 1) / rt);
     const int64_t max_units = ((int64_t)c.max_pages * c.T + qup::kCacheUnit - 1) / qup::kCacheUnit;
     // the chunk kernel counts steps in 32 bits
     if (chunk && ((int64_t)c.max_pages * c.T + 256 + max_q) * g + 256 >= ((int64_t)1 << 31)) return QUP_ERR_ARG;
@@ -168,7 +169,7 @@ int qup_cache_attn(const qup_cache* cache, const void* Q, int64_t q_stride, cons
 
     qup::DeviceInfo dev;
     if ((rc = qup::device_info(&dev))) return rc;
-    const int ctas = std::min(2 * dev.sms, qup::kCacheMaxCtas);
+    const int ctas = std::min(dev.sms, qup::kCacheMaxSms) * qup::cache_attn_ctas(nt);
     int grid = ctas;
     p.nsplit = 1;
     if (sparse) {
@@ -178,7 +179,7 @@ int qup_cache_attn(const qup_cache* cache, const void* Q, int64_t q_stride, cons
         p.list_cap = (int)((entries + p.nsplit - 1) / p.nsplit);
         grid = (int)(items * p.nsplit);
     }
-    if (qup::cache_attn_smem(mt, sparse, c.max_pages, p.list_cap) > (size_t)dev.smem_optin ||
+    if (qup::cache_attn_smem(nt, sparse, c.max_pages, p.list_cap) > (size_t)dev.smem_optin ||
         qup::cache_chunk_smem() > (size_t)dev.smem_optin)
         return QUP_ERR_ARG;
 
@@ -230,7 +231,7 @@ int qup_cache_attn(const qup_cache* cache, const void* Q, int64_t q_stride, cons
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (chunk && qup::launch_cache_chunk(tmc[0], tmc[1], p, std::min(dev.sms, qup::kChunkMaxRuns), st) != cudaSuccess)
         return QUP_ERR_CUDA;
-    if (small && qup::launch_cache_attn(mt, tm[0], tm[1], p, grid, (int)items, st) != cudaSuccess) return QUP_ERR_CUDA;
+    if (small && qup::launch_cache_attn(nt, tm[0], tm[1], p, grid, (int)items, st) != cudaSuccess) return QUP_ERR_CUDA;
     if (page_weight && qup::launch_cache_weights(p, st) != cudaSuccess) return QUP_ERR_CUDA;
     return QUP_OK;
 }

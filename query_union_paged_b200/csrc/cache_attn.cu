@@ -13,11 +13,14 @@
 //
 // Layout: a work unit is 64 tokens of one KV head: 8 KB of K and 8 KB of V, streamed by one
 // producer warp with TMA (128-byte swizzle) through a ring of stages.  Each of the four consumer
-// warps takes 16 tokens of every unit, two units at a time, with its own running maximum, sum and output (no exchange
-// inside the loop), 16 or 32 rows per tile as mma.m16n8k16 operands straight from the bytes: the
-// order of d inside K's fragments and of d over the output columns is free, so every lane reads 16
-// consecutive bytes of a token (conflict-free under the swizzle) and converts two values at a time.
-// The warps merge in shared memory at the end of a segment.
+// warps takes 16 tokens of every unit, two units at a time, with its own running maximum, sum and output
+// (no exchange inside the loop).  Tokens are the rows of the products and query rows their columns:
+// S^T = K Q^T and O^T = V^T P^T as mma.m16n8k16, so 8 rows cost no more than one and the cache's bytes are
+// operands as they lie: the order of d inside K's fragments and of d over the output rows is free, every
+// lane reads 16 consecutive bytes of a token (conflict-free under the swizzle) and converts two
+// values at a time; P^T is turned by movmatrix.  (With query rows as the products' rows a tile is 16 high:
+// twice the products and exponentials for 4 heads, 437 instructions for 16 tokens.)  The warps merge
+// in shared memory at the end of a segment.
 //
 // Work split: all pages: the units of all (request, KV head, row tile) items are laid end to end and
 // cut into equal runs, one per CTA, so ragged lengths balance; an item cut across CTAs leaves one
@@ -73,6 +76,11 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t* a, uint3
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {  // an 8 x 8 matrix of 16-bit elements over the warp
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
 }
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
     uint4 v;
@@ -203,25 +211,27 @@ struct Cursor {
 };
 
 // Shared memory, from a 1024-byte boundary: the ring, then what follows.
-template <int MT>
+// NT: row tiles of 8 rows.  Up to 8 rows leave registers for three CTAs on an SM (four stages each).
+template <int NT>
 struct Smem {
-    static constexpr int RT = 16 * MT;
-    static constexpr int kStages = MT == 1 ? 6 : 5;
+    static constexpr int RT = 8 * NT;
+    static constexpr int kStages = NT == 1 ? 4 : 6;
     static constexpr uint32_t ring = 0;
     static constexpr uint32_t out = ring + kStages * 2 * kTile;             // [RT][128] fp32
-    static constexpr uint32_t qfrag = out + RT * kHeadDim * 4;  // [MT][8][32] uint4
-    static constexpr uint32_t meta = qfrag + RT * kHeadDim * 2;  // [kStages][kMaxBoxes]
+    static constexpr uint32_t qfrag = out + RT * kHeadDim * 4;  // NT = 4: [NT][8][32] uint2
+    static constexpr uint32_t meta = qfrag + (NT == 4 ? RT * kHeadDim * 2 : 0);  // [kStages][kMaxBoxes]
     static constexpr uint32_t ml = meta + kStages * kMaxBoxes * sizeof(PageMeta);  // [kConsumers][RT] float2
     static constexpr uint32_t bars = ml + kConsumers * RT * 8;
     static constexpr uint32_t misc = bars + 2 * kStages * 8;  // abort flag, start, scan
     static constexpr uint32_t list = misc + 64 + 64;  // TopK: bitmap, prefix, pages, masks
 };
 
-template <int MT, bool SPARSE, bool WEIGHTS>
-__global__ void __launch_bounds__(kThreads, MT == 1 ? 2 : 1)
+template <int NT, bool SPARSE, bool WEIGHTS>
+__global__ void __launch_bounds__(kThreads, cache_attn_ctas(NT))
     cache_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const __grid_constant__ CacheAttnParams p) {
-    using L = Smem<MT>;
+    using L = Smem<NT>;
+    constexpr bool kQRegs = NT < 4;  // Q stays in registers
     constexpr int RT = L::RT, NS = L::kStages;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -458,67 +468,73 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 2 : 1)
     const int i = lane >> 2, q4 = lane & 3;
     float* s_out = reinterpret_cast<float*>(smem + L::out);
     float2* s_ml = reinterpret_cast<float2*>(smem + L::ml);
-    uint4* s_q = reinterpret_cast<uint4*>(smem + L::qfrag);
+    uint2* s_q = reinterpret_cast<uint2*>(smem + L::qfrag);
     bool first_seg = true;
     while (SPARSE ? more : cur.next(p, RT, sg)) {
         more = false;
         const int rows = SPARSE ? g : min(RT, sg.n * g - sg.tile * RT);  // rows of the tile
         const int row0 = SPARSE ? 0 : sg.tile * RT;                     // in (query, head) order
         const int e0 = sg.b0, e1 = min(sg.b1, sg.nvis);
-        // ---- Q fragments: lane (i, q4) holds d = 32 q4 + 4 ks .. + 3 of rows i and i + 8
-        float rs[MT][2];
-        int vis[MT][2];  // tokens each row sees
-        float m[MT][2], l[MT][2], o[MT][16][4];
-        bar_sync(1, 32 * kConsumers);  // the last segment's fragments are done with
+        // ---- Q as B operand: lane (i, q4) holds d = 32 q4 + 4 ks .. + 3 of row 8 t + i
+        uint32_t qb[kQRegs ? NT : 1][8][2];
+        float rs[NT][2];  // of rows 8 t + 2 q4, + 1: score factor, tokens they see, maximum, sum
+        int vis[NT][2];
+        float m[NT][2], l[NT][2], o[NT][8][4];
+        if (!kQRegs) bar_sync(1, 32 * kConsumers);  // the last segment's are done with
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            uint32_t f[8][4];
+        for (int t = 0; t < NT; ++t) {
+            const int rr = 8 * t + i;
+            const bool on = rr < rows;
+            const int x = row0 + (on ? rr : 0), qi = SPARSE ? 0 : x / g, j = x - qi * g;
+            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.Q) +
+                                                              (size_t)(sg.q0 + qi) * p.q_stride +
+                                                              (size_t)(sg.h * g + j) * kHeadDim + 32 * q4);
+            uint4 raw[4];
+            uint32_t top = 0;
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                const int rr = 16 * mt + 8 * hf + i;
-                const bool on = rr < rows;
-                const int x = row0 + (on ? rr : 0), qi = SPARSE ? 0 : x / g, j = x - qi * g;
-                const uint4* src = reinterpret_cast<const uint4*>(
-                    static_cast<const uint16_t*>(p.Q) + (size_t)(sg.q0 + qi) * p.q_stride +
-                    (size_t)(sg.h * g + j) * kHeadDim + 32 * q4);
-                uint4 raw[4];
-                uint32_t top = 0;
+            for (int u = 0; u < 4; ++u) {
+                raw[u] = on ? __ldg(src + u) : make_uint4(0u, 0u, 0u, 0u);
+                const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    raw[u] = on ? __ldg(src + u) : make_uint4(0u, 0u, 0u, 0u);
-                    const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) top = max(top, max((w[e] << 16) & 0x7f800000u, w[e] & 0x7f800000u));
-                }
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                // the row's largest element is in [2^e, 2^(e+1)): times 2^(14 - e)
-                const int ex = max((int)(top >> 23) - 127, -100);
-                const float up = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
-                rs[mt][hf] = p.scale_log2 * __uint_as_float((uint32_t)(ex - 14 + 127) << 23);
-                vis[mt][hf] = on ? (SPARSE ? sg.len : sg.len - sg.n + qi + 1) : 0;
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)  // word 4u + e: k-step 2u + e / 2, register half e & 1
-                        f[2 * u + e / 2][hf + 2 * (e & 1)] = pack_f16x2(__uint_as_float(w[e] << 16) * up,
-                                                                       __uint_as_float(w[e] & 0xffff0000u) * up);
-                }
-                m[mt][hf] = kNegInf;
-                l[mt][hf] = 0.f;
+                for (int e = 0; e < 4; ++e) top = max(top, max((w[e] << 16) & 0x7f800000u, w[e] & 0x7f800000u));
             }
-            if (warp == mt) {
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // the row's largest element is in [2^e, 2^(e+1)): times 2^(14 - e)
+            const int ex = max((int)(top >> 23) - 127, -100);
+            const float up = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
+            const float row_rs = p.scale_log2 * __uint_as_float((uint32_t)(ex - 14 + 127) << 23);
+            const int row_vis = on ? (SPARSE ? sg.len : sg.len - sg.n + qi + 1) : 0;
 #pragma unroll
-                for (int s = 0; s < 8; ++s)
-                    s_q[(mt * 8 + s) * 32 + lane] = make_uint4(f[s][0], f[s][1], f[s][2], f[s][3]);
+            for (int u = 0; u < 4; ++u) {
+                const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {  // words 4 u + e, + 1: k-step 2 u + e / 2
+                    const uint32_t b0 = pack_f16x2(__uint_as_float(w[e] << 16) * up,
+                                                   __uint_as_float(w[e] & 0xffff0000u) * up);
+                    const uint32_t b1 = pack_f16x2(__uint_as_float(w[e + 1] << 16) * up,
+                                                   __uint_as_float(w[e + 1] & 0xffff0000u) * up);
+                    if constexpr (kQRegs) {
+                        qb[t][2 * u + e / 2][0] = b0;
+                        qb[t][2 * u + e / 2][1] = b1;
+                    } else if (warp == t) {
+                        s_q[(t * 8 + 2 * u + e / 2) * 32 + lane] = make_uint2(b0, b1);
+                    }
+                }
             }
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
+            for (int e = 0; e < 2; ++e) {  // lane 4 y holds row 8 t + y
+                rs[t][e] = __shfl_sync(0xffffffffu, row_rs, 4 * (2 * q4 + e));
+                vis[t][e] = __shfl_sync(0xffffffffu, row_vis, 4 * (2 * q4 + e));
+                m[t][e] = kNegInf;
+                l[t][e] = 0.f;
+            }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[mt][j][e] = 0.f;
+            for (int d = 0; d < 8; ++d)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[t][d][e] = 0.f;
         }
-        bar_sync(1, 32 * kConsumers);
+        if (!kQRegs) bar_sync(1, 32 * kConsumers);
         // tokens that every row of the tile sees, and that any row sees
         const int vis_all = SPARSE ? sg.len : sg.len - sg.n + row0 / g + 1;
         const int vis_any = SPARSE ? sg.len : sg.len - sg.n + (row0 + rows - 1) / g + 1;
@@ -551,98 +567,114 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 2 : 1)
             }
             if (dead) return;
             if (any) {
-                // ---- S = Q K^T: token 8 nt + i of the warp, d = 32 q4 .. + 31 of it in two loads
-                float c[NG][MT][2][4];
+                // ---- S^T = K Q^T: tokens i and i + 8 of the warp, d = 32 q4 .. + 31 of each in two loads
+                float c[NG][NT][4];
 #pragma unroll
                 for (int n = 0; n < NG; ++n)
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
+                    for (int t = 0; t < NT; ++t)
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) c[n][mt][e >> 2][e & 3] = 0.f;
+                        for (int e = 0; e < 4; ++e) c[n][t][e] = 0.f;
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
                     uint4 k[NG][2];
 #pragma unroll
                     for (int n = 0; n < NG; ++n)
 #pragma unroll
-                        for (int nt = 0; nt < 2; ++nt)
-                            k[n][nt] = lds128(tile[n] + (16 * warp + 8 * nt + i) * kHeadDim + (((2 * q4 + s) ^ i) << 4));
+                        for (int y = 0; y < 2; ++y)
+                            k[n][y] = lds128(tile[n] + (16 * warp + 8 * y + i) * kHeadDim + (((2 * q4 + s) ^ i) << 4));
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        uint32_t aw[MT][4];
+                        uint32_t b[NT][2];
 #pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) {
-                            const uint4 a = s_q[(mt * 8 + 4 * s + e) * 32 + lane];
-                            aw[mt][0] = a.x;
-                            aw[mt][1] = a.y;
-                            aw[mt][2] = a.z;
-                            aw[mt][3] = a.w;
+                        for (int t = 0; t < NT; ++t) {
+                            if constexpr (kQRegs) {
+                                b[t][0] = qb[t][4 * s + e][0];
+                                b[t][1] = qb[t][4 * s + e][1];
+                            } else {
+                                const uint2 v = s_q[(t * 8 + 4 * s + e) * 32 + lane];
+                                b[t][0] = v.x;
+                                b[t][1] = v.y;
+                            }
                         }
 #pragma unroll
-                        for (int n = 0; n < NG; ++n)
+                        for (int n = 0; n < NG; ++n) {
+                            uint32_t a[4];
 #pragma unroll
-                            for (int nt = 0; nt < 2; ++nt) {
-                                const uint32_t w = e < 2 ? (e == 0 ? k[n][nt].x : k[n][nt].y)
-                                                         : (e == 2 ? k[n][nt].z : k[n][nt].w);
-                                const uint32_t b0 = cvt_e4m3x2(w), b1 = cvt_e4m3x2(w >> 16);
-#pragma unroll
-                                for (int mt = 0; mt < MT; ++mt) mma16816(c[n][mt][nt], aw[mt], b0, b1);
+                            for (int y = 0; y < 2; ++y) {
+                                const uint32_t w = e < 2 ? (e == 0 ? k[n][y].x : k[n][y].y)
+                                                         : (e == 2 ? k[n][y].z : k[n][y].w);
+                                a[y] = cvt_e4m3x2(w);
+                                a[y + 2] = cvt_e4m3x2(w >> 16);
                             }
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) mma16816(c[n][t], a, b[t][0], b[t][1]);
+                        }
                     }
                 }
-                uint32_t pa[NG][MT][4];
+                uint32_t pb[NG][NT][2];
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
+                for (int t = 0; t < NT; ++t) {
+                    float x[NG][4], bm[2] = {kNegInf, kNegInf};
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        const int rr = 16 * mt + 8 * hf + i;
-                        float x[NG][4], bm = kNegInf;
+                    for (int n = 0; n < NG; ++n) {
+                        // c: token i of rows 2 q4, + 1, then token i + 8 of them
 #pragma unroll
-                        for (int n = 0; n < NG; ++n) {
-                            const float f = rs[mt][hf] * pm[n].ks;
+                        for (int e = 0; e < 4; ++e) x[n][e] = fmaf(c[n][t][e], rs[t][e & 1] * pm[n].ks, pm[n].vs_log2);
+                        if (mixed[n]) {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                x[n][e] = fmaf(c[n][mt][e >> 1][2 * hf + (e & 1)], f, pm[n].vs_log2);
-                            if (mixed[n]) {
-                                const bool on = live[n] && (!SPARSE || ((pm[n].mask >> (rr & 31)) & 1u));
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    if (!on || pos[n] + 8 * (e >> 1) + 2 * q4 + (e & 1) >= vis[mt][hf]) x[n][e] = kNegInf;
-                            }
-                            bm = fmaxf(bm, fmaxf(fmaxf(x[n][0], x[n][1]), fmaxf(x[n][2], x[n][3])));
-                        }
-                        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 1));
-                        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 2));
-                        if (__any_sync(0xffffffffu, bm > m[mt][hf] + kLazy)) {
-                            const bool mv = bm > m[mt][hf] + kLazy;  // -inf + kLazy = -inf
-                            const float a = mv ? ex2(m[mt][hf] - bm) : 1.f;
-                            if (mv) m[mt][hf] = bm;
-                            l[mt][hf] *= a;
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                o[mt][j][2 * hf] *= a;
-                                o[mt][j][2 * hf + 1] *= a;
+                            for (int e = 0; e < 4; ++e) {
+                                const bool on = live[n] && (!SPARSE || ((pm[n].mask >> (8 * t + 2 * q4 + (e & 1))) & 1u));
+                                if (!on || pos[n] + i + 8 * (e >> 1) >= vis[t][e & 1]) x[n][e] = kNegInf;
                             }
                         }
-                        const float sub = m[mt][hf] == kNegInf ? 0.f : m[mt][hf] - kOffset;
 #pragma unroll
-                        for (int n = 0; n < NG; ++n) {
+                        for (int e = 0; e < 2; ++e) bm[e] = fmaxf(bm[e], fmaxf(x[n][e], x[n][e + 2]));
+                    }
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) x[n][e] = ex2(x[n][e] - sub);
-                            float sum = ((x[n][0] + x[n][1]) + (x[n][2] + x[n][3])) * pm[n].vs_inv;
-                            l[mt][hf] += sum;
+                    for (int o2 = 4; o2 < 32; o2 *= 2)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) bm[e] = fmaxf(bm[e], __shfl_xor_sync(0xffffffffu, bm[e], o2));
+                    if (__any_sync(0xffffffffu, bm[0] > m[t][0] + kLazy || bm[1] > m[t][1] + kLazy)) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const bool mv = bm[e] > m[t][e] + kLazy;  // -inf + kLazy = -inf
+                            const float a = mv ? ex2(m[t][e] - bm[e]) : 1.f;
+                            if (mv) m[t][e] = bm[e];
+                            l[t][e] *= a;
+#pragma unroll
+                            for (int d = 0; d < 8; ++d) {
+                                o[t][d][e] *= a;
+                                o[t][d][e + 2] *= a;
+                            }
+                        }
+                    }
+                    float sub[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) sub[e] = m[t][e] == kNegInf ? 0.f : m[t][e] - kOffset;
+#pragma unroll
+                    for (int n = 0; n < NG; ++n) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[n][e] = ex2(x[n][e] - sub[e & 1]);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float sum = (x[n][e] + x[n][e + 2]) * pm[n].vs_inv;
+                            l[t][e] += sum;
                             if constexpr (WEIGHTS) {
-                                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                                if (q4 == 0 && rr < rows && pos[n] < vis_any)
-                                    mass[(size_t)(pos[n] / 16) * mass_rows + rr] = make_float2(sum, m[mt][hf]);
+#pragma unroll
+                                for (int o2 = 4; o2 < 32; o2 *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o2);
+                                const int rr = 8 * t + 2 * q4 + e;
+                                if (i == 0 && rr < rows && pos[n] < vis_any)
+                                    mass[(size_t)(pos[n] / 16) * mass_rows + rr] = make_float2(sum, m[t][e]);
                             }
-                            pa[n][mt][hf] = pack_f16x2(x[n][0], x[n][1]);
-                            pa[n][mt][hf + 2] = pack_f16x2(x[n][2], x[n][3]);
                         }
+                        // P^T as B operand: rows to lanes, tokens to registers
+                        pb[n][t][0] = transpose8(pack_f16x2(x[n][0], x[n][1]));
+                        pb[n][t][1] = transpose8(pack_f16x2(x[n][2], x[n][3]));
                     }
                 }
-                // ---- O += P V: tokens 2 q4, + 1, + 8, + 9 of the warp, d = 16 i .. + 15 of each
+                // ---- O^T += V^T P^T: tokens 2 q4, + 1, + 8, + 9 of the warp, d = 16 i .. + 15 of each; product
+                // 2 w + hi takes d = 16 i + 4 w + 2 hi and the one after it
 #pragma unroll
                 for (int n = 0; n < NG; ++n) {
                     uint32_t v[4][4];
@@ -669,56 +701,52 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 2 : 1)
                         }
                         slow = __any_sync(0xffffffffu, nan);
                     }
+                    const auto operand = [](const uint32_t (&v)[4][4], int w, int hi, uint32_t (&a)[4]) {
+                        const uint32_t x0 = __byte_perm(v[0][w], v[1][w], hi ? 0x7362 : 0x5140);
+                        const uint32_t x1 = __byte_perm(v[2][w], v[3][w], hi ? 0x7362 : 0x5140);
+                        a[0] = cvt_e4m3x2(x0);
+                        a[1] = cvt_e4m3x2(x0 >> 16);
+                        a[2] = cvt_e4m3x2(x1);
+                        a[3] = cvt_e4m3x2(x1 >> 16);
+                    };
                     if (!slow) {
 #pragma unroll
-                        for (int w = 0; w < 4; ++w) {
+                        for (int w = 0; w < 4; ++w)
 #pragma unroll
                             for (int hi = 0; hi < 2; ++hi) {
-                                const uint32_t x0 = __byte_perm(v[0][w], v[1][w], hi ? 0x7362 : 0x5140);
-                                const uint32_t x1 = __byte_perm(v[2][w], v[3][w], hi ? 0x7362 : 0x5140);
+                                uint32_t a[4];
+                                operand(v, w, hi, a);
 #pragma unroll
-                                for (int d = 0; d < 2; ++d) {
-                                    const uint32_t b0 = cvt_e4m3x2(d ? x0 >> 16 : x0), b1 = cvt_e4m3x2(d ? x1 >> 16 : x1);
-#pragma unroll
-                                    for (int mt = 0; mt < MT; ++mt) mma16816(o[mt][4 * w + 2 * hi + d], pa[n][mt], b0, b1);
-                                }
+                                for (int t = 0; t < NT; ++t) mma16816(o[t][2 * w + hi], a, pb[n][t][0], pb[n][t][1]);
                             }
-                        }
                     } else {
                         // row by row: the other rows' weights and the tokens the row does not see are zero
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
 #pragma unroll 1
-                        for (int rr = 0; rr < rows; ++rr) {
-                            const int rv = SPARSE ? sg.len : sg.len - sg.n + (row0 + rr) / g + 1;
-                            const bool on = !SPARSE || ((pm[n].mask >> rr) & 1u);
-                            const int mine_mt = rr >> 4, mine_hf = (rr >> 3) & 1;
-                            const bool own = (rr & 7) == i;
-                            uint32_t a[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                uint32_t x = pa[n][0][e];
-                                if (MT > 1 && mine_mt == 1) x = pa[n][MT - 1][e];
-                                a[e] = own && (e & 1) == mine_hf ? x : 0u;
-                            }
-#pragma unroll
-                            for (int w = 0; w < 4; ++w) {
-                                uint32_t z[4];
+                            for (int y = 0; y < 8 && 8 * t + y < rows; ++y) {
+                                const int rr = 8 * t + y, rv = SPARSE ? sg.len : sg.len - sg.n + (row0 + rr) / g + 1;
+                                const bool on = !SPARSE || ((pm[n].mask >> rr) & 1u);
+                                uint32_t z[4][4];
 #pragma unroll
                                 for (int e = 0; e < 4; ++e)
-                                    z[e] = on && pos[n] + 2 * q4 + (e & 1) + 8 * (e >> 1) < rv ? v[e][w] : 0u;
 #pragma unroll
-                                for (int d = 0; d < 4; ++d) {
-                                    const uint32_t x0 = __byte_perm(z[0], z[1], d < 2 ? 0x5140 : 0x7362);
-                                    const uint32_t x1 = __byte_perm(z[2], z[3], d < 2 ? 0x5140 : 0x7362);
-                                    float t[4] = {0.f, 0.f, 0.f, 0.f};
-                                    mma16816(t, a, cvt_e4m3x2(d & 1 ? x0 >> 16 : x0), cvt_e4m3x2(d & 1 ? x1 >> 16 : x1));
+                                    for (int w = 0; w < 4; ++w)
+                                        z[e][w] = on && pos[n] + 2 * q4 + (e & 1) + 8 * (e >> 1) < rv ? v[e][w] : 0u;
+                                const uint32_t b0 = y == i ? pb[n][t][0] : 0u, b1 = y == i ? pb[n][t][1] : 0u;
 #pragma unroll
-                                    for (int mt = 0; mt < MT; ++mt)
+                                for (int w = 0; w < 4; ++w)
+#pragma unroll
+                                    for (int hi = 0; hi < 2; ++hi) {
+                                        uint32_t a[4];
+                                        operand(z, w, hi, a);
+                                        float r4[4] = {0.f, 0.f, 0.f, 0.f};
+                                        mma16816(r4, a, b0, b1);
 #pragma unroll
                                         for (int e = 0; e < 4; ++e)
-                                            if (own && mt == mine_mt && (e >> 1) == mine_hf) o[mt][4 * w + d][e] += t[e];
-                                }
+                                            if (2 * q4 + (e & 1) == y) o[t][2 * w + hi][e] += r4[e];
+                                    }
                             }
-                        }
                     }
                 }
             } else if (WEIGHTS) {
@@ -735,46 +763,42 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 2 : 1)
             it += NG;
         };
         int b = e0;
-        if (MT == 1)
+        if (NT < 4)
             for (; b + 1 < e1 && !dead; b += 2) turn(std::integral_constant<int, 2>());
         for (; b < e1 && !dead; ++b) turn(std::integral_constant<int, 1>());
 
         // ---- the four warps' results, joined
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                l[mt][hf] += __shfl_xor_sync(0xffffffffu, l[mt][hf], 1);
-                l[mt][hf] += __shfl_xor_sync(0xffffffffu, l[mt][hf], 2);
-                if (q4 == 0) s_ml[warp * RT + 16 * mt + 8 * hf + i] = make_float2(m[mt][hf], l[mt][hf]);
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int o2 = 4; o2 < 32; o2 *= 2) l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], o2);
+                if (i == 0) s_ml[warp * RT + 8 * t + 2 * q4 + e] = make_float2(m[t][e], l[t][e]);
             }
         bar_sync(1, 32 * kConsumers);
 #pragma unroll 1
         for (int w = 0; w < kConsumers; ++w) {
             if (warp == w) {
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
+                for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        const int rr = 16 * mt + 8 * hf + i;
+                    for (int e = 0; e < 2; ++e) {
+                        const int rr = 8 * t + 2 * q4 + e;
                         float M = kNegInf;
 #pragma unroll
                         for (int x = 0; x < kConsumers; ++x) M = fmaxf(M, s_ml[x * RT + rr].x);
-                        const float f = m[mt][hf] == kNegInf ? 0.f : ex2(m[mt][hf] - M);
-                        // d = 16 (2 q4 + e) + j: 16 consecutive floats, stored as four float4 in an order
-                        // that spreads the lanes of a row over the banks
+                        const float f = m[t][e] == kNegInf ? 0.f : ex2(m[t][e] - M);
+                        // d = 16 i + 4 j .. + 3
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                float4* dst = reinterpret_cast<float4*>(s_out + rr * kHeadDim + 16 * (2 * q4 + e)) + j;
-                                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-                                if (w > 0) x = *dst;
-                                const float a0 = o[mt][4 * j][2 * hf + e], a1 = o[mt][4 * j + 1][2 * hf + e],
-                                            a2 = o[mt][4 * j + 2][2 * hf + e], a3 = o[mt][4 * j + 3][2 * hf + e];
-                                // a warp that saw nothing adds nothing (its factor 0 times 0)
-                                *dst = make_float4(x.x + a0 * f, x.y + a1 * f, x.z + a2 * f, x.w + a3 * f);
-                            }
+                        for (int j = 0; j < 4; ++j) {
+                            float4* dst = reinterpret_cast<float4*>(s_out + rr * kHeadDim + 16 * i) + j;
+                            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (w > 0) x = *dst;
+                            // a warp that saw nothing adds nothing (its factor 0 times 0)
+                            *dst = make_float4(x.x + o[t][2 * j][e] * f, x.y + o[t][2 * j][e + 2] * f,
+                                               x.z + o[t][2 * j + 1][e] * f, x.w + o[t][2 * j + 1][e + 2] * f);
+                        }
                     }
             }
             bar_sync(1, 32 * kConsumers);
@@ -1004,45 +1028,49 @@ __global__ void __launch_bounds__(32 * kWeightWarps) cache_weight_kernel(const _
     }
 }
 
-template <int MT, bool SPARSE, bool WEIGHTS>
+template <int NT, bool SPARSE, bool WEIGHTS>
 cudaError_t launch_main(const CUtensorMap& tmK, const CUtensorMap& tmV, const CacheAttnParams& p, int grid,
                         cudaStream_t stream) {
-    const size_t smem = cache_attn_smem(MT, SPARSE, p.max_pages, p.list_cap);
-    const cudaError_t e = ensure_smem_attr((const void*)cache_attn_kernel<MT, SPARSE, WEIGHTS>, smem);
+    const size_t smem = cache_attn_smem(NT, SPARSE, p.max_pages, p.list_cap);
+    const cudaError_t e = ensure_smem_attr((const void*)cache_attn_kernel<NT, SPARSE, WEIGHTS>, smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(cache_attn_kernel<MT, SPARSE, WEIGHTS>, dim3(grid), dim3(kThreads), smem, stream, tmK, tmV, p);
+    return launch_pdl(cache_attn_kernel<NT, SPARSE, WEIGHTS>, dim3(grid), dim3(kThreads), smem, stream, tmK, tmV, p);
 }
 
-// TopK pages: 16 or 32 rows (the heads of a KV head); all pages: 16 rows, more are the chunk kernel's.
-template <int MT>
+template <int NT>
 cudaError_t launch_sparse(const CUtensorMap& tmK, const CUtensorMap& tmV, const CacheAttnParams& p, int grid, int items,
                           cudaStream_t stream) {
-    const cudaError_t e = p.weight ? launch_main<MT, true, true>(tmK, tmV, p, grid, stream)
-                                   : launch_main<MT, true, false>(tmK, tmV, p, grid, stream);
+    const cudaError_t e = p.weight ? launch_main<NT, true, true>(tmK, tmV, p, grid, stream)
+                                   : launch_main<NT, true, false>(tmK, tmV, p, grid, stream);
     if (e != cudaSuccess || p.nsplit == 1) return e;
-    return launch_pdl(cache_merge_kernel<16 * MT, true>, dim3(items), dim3(kHeadDim), 0, stream, p, grid);
+    return launch_pdl(cache_merge_kernel<8 * NT, true>, dim3(items), dim3(kHeadDim), 0, stream, p, grid);
 }
 
+template <int NT>
 cudaError_t launch_dense(const CUtensorMap& tmK, const CUtensorMap& tmV, const CacheAttnParams& p, int grid, int items,
                          cudaStream_t stream) {
-    const cudaError_t e = p.weight ? launch_main<1, false, true>(tmK, tmV, p, grid, stream)
-                                   : launch_main<1, false, false>(tmK, tmV, p, grid, stream);
+    const cudaError_t e = p.weight ? launch_main<NT, false, true>(tmK, tmV, p, grid, stream)
+                                   : launch_main<NT, false, false>(tmK, tmV, p, grid, stream);
     if (e != cudaSuccess) return e;
-    return launch_pdl(cache_merge_kernel<16, false>, dim3(items), dim3(kHeadDim), 0, stream, p, grid);
+    return launch_pdl(cache_merge_kernel<8 * NT, false>, dim3(items), dim3(kHeadDim), 0, stream, p, grid);
 }
 
 }  // namespace
 
-size_t cache_attn_smem(int mt, bool sparse, int max_pages, int list_cap) {
-    size_t s = mt == 1 ? Smem<1>::list : Smem<2>::list;
+size_t cache_attn_smem(int nt, bool sparse, int max_pages, int list_cap) {
+    size_t s = nt == 1 ? Smem<1>::list : (nt == 2 ? Smem<2>::list : Smem<4>::list);
     if (sparse) s += (size_t)((max_pages + 31) / 32) * 8 + (size_t)list_cap * 8;
     return s + 1024;
 }
 
-cudaError_t launch_cache_attn(int mt, const CUtensorMap& tmK, const CUtensorMap& tmV, const CacheAttnParams& p,
+cudaError_t launch_cache_attn(int nt, const CUtensorMap& tmK, const CUtensorMap& tmV, const CacheAttnParams& p,
                               int grid, int items, cudaStream_t stream) {
-    if (!p.topk) return launch_dense(tmK, tmV, p, grid, items, stream);
-    return mt == 1 ? launch_sparse<1>(tmK, tmV, p, grid, items, stream) : launch_sparse<2>(tmK, tmV, p, grid, items, stream);
+    if (!p.topk)  // up to 16 rows: more are the chunk kernel's
+        return nt == 1 ? launch_dense<1>(tmK, tmV, p, grid, items, stream)
+                       : launch_dense<2>(tmK, tmV, p, grid, items, stream);
+    return nt == 1   ? launch_sparse<1>(tmK, tmV, p, grid, items, stream)
+           : nt == 2 ? launch_sparse<2>(tmK, tmV, p, grid, items, stream)
+                     : launch_sparse<4>(tmK, tmV, p, grid, items, stream);
 }
 
 cudaError_t launch_cache_weights(const CacheAttnParams& p, cudaStream_t stream) {

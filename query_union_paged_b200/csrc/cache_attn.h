@@ -12,11 +12,14 @@
 namespace qup {
 
 constexpr int kCacheUnit = 64;       // tokens of a work unit
-constexpr int kCacheMaxCtas = 296;   // CTAs that leave partial results: two on each of 148 SMs
-constexpr int kCacheMaxRows = 32;    // rows of the widest row tile
+constexpr int kCacheMaxSms = 148;
+// CTAs of the small kernel on an SM, by its row tiles of 8 rows
+__host__ __device__ constexpr int cache_attn_ctas(int nt) { return nt == 1 ? 3 : (nt == 2 ? 2 : 1); }
+// rows of partial results: two tiles of every CTA (8 rows x 3 CTAs, 16 x 2 or 32 x 1 on an SM)
+constexpr int kCachePartRows = 2 * 32 * kCacheMaxSms;
 constexpr int kCacheSmallRows = 16;  // rows (queries x heads of a KV head) up to which a request is a small one
 constexpr int kChunkRows = 256;      // rows of an item of the other kernel (cache_chunk.cu)
-constexpr int kChunkMaxRuns = 148;   // and its CTAs
+constexpr int kChunkMaxRuns = kCacheMaxSms;   // and its CTAs
 
 // What a CTA of the chunk kernel worked on: its last item, from which step, whether the item ends
 // with it, and the first item's end.
@@ -54,10 +57,10 @@ struct CacheAttnParams {
     int list_cap;    // TopK pages: distinct pages of one CTA, at most
 };
 
-// mt: row tiles of 16 * mt rows (1 or 2)
-size_t cache_attn_smem(int mt, bool sparse, int max_pages, int list_cap);
+// nt: row tiles of 8 rows (1, 2 or 4)
+size_t cache_attn_smem(int nt, bool sparse, int max_pages, int list_cap);
 // items: (request, KV head, row tile) triples of max_tiles each, or (query, KV head) pairs
-cudaError_t launch_cache_attn(int mt, const CUtensorMap& tmK, const CUtensorMap& tmV, const CacheAttnParams& p,
+cudaError_t launch_cache_attn(int nt, const CUtensorMap& tmK, const CUtensorMap& tmV, const CacheAttnParams& p,
                               int grid, int items, cudaStream_t stream);
 // the requests of big_rows or more; tensor maps with boxes of a whole page
 size_t cache_chunk_smem();
