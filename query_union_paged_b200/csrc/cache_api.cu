@@ -106,7 +106,7 @@ int qup_cache_append(const qup_cache* cache, const void* k_new, const void* v_ne
     if (N == 0 || cache->R == 0) return QUP_OK;
     if (check_cache_pointers(cache) || !k_new || !v_new || !tok_ptr) return QUP_ERR_ARG;
     if ((reinterpret_cast<uintptr_t>(k_new) | reinterpret_cast<uintptr_t>(v_new)) & 15) return QUP_ERR_ARG;
-    if ((int64_t)N / cache->T + 2 * (int64_t)cache->R >= ((int64_t)1 << 31) - 1) return QUP_ERR_ARG;
+    if (((int64_t)N / cache->T + 2 * (int64_t)cache->R) * 2 * cache->Hkv >= ((int64_t)1 << 31)) return QUP_ERR_ARG;
     qup::DeviceInfo dev;
     if ((rc = qup::device_info(&dev))) return rc;
     return qup::launch_cache_append(view_of(cache), k_new, v_new, dtype == QUP_BF16, k_stride, v_stride, tok_ptr, N,
@@ -175,6 +175,8 @@ int qup_cache_attn(const qup_cache* cache, const void* Q, int64_t q_stride, cons
     if (sparse) {
         const int64_t entries = std::min<int64_t>((int64_t)g * Ksel, c.max_pages);
         const int64_t units = std::max<int64_t>((entries * c.T + qup::kCacheUnit - 1) / qup::kCacheUnit, 1);
+        // as many CTAs as the SMs hold at once: finding its pages costs a CTA what 8 units do, so more
+        // and shorter ones lose (32 x 32K, 32 of 64-token pages: 41 us with one CTA a pair, 55 with four)
         p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>(ctas / items, units));
         p.list_cap = (int)((entries + p.nsplit - 1) / p.nsplit);
         grid = (int)(items * p.nsplit);

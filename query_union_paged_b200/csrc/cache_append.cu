@@ -10,7 +10,9 @@
 // One CTA per run of a request's tokens inside one page, for some of its units (K or V of a KV head).  A
 // unit's tokens are read once into registers (16 bytes a load), their largest finite magnitude is
 // reduced over the CTA, and the registers are scaled, rounded (nearest even) and written; the next
-// unit's loads are under way meanwhile.  Bound by DRAM: N * Hkv * 128 * (element + 1) bytes for each of
+// unit's loads are under way meanwhile.  A run without infinities and NaN takes the short way: two
+// magnitudes an instruction, no test of each value (with them the kernel was bound by its instructions,
+// 3.4 TB/s).  Bound by DRAM: N * Hkv * 128 * (element + 1) bytes for each of
 // K and V.
 #include <algorithm>
 #include <cstdint>
@@ -60,6 +62,17 @@ __device__ __forceinline__ uint32_t pack_e4m3_checked(const float* x) {
     return w;
 }
 
+// The CTA's maximum; `part` holds one entry per warp.
+template <int WARPS>
+__device__ __forceinline__ uint32_t cta_max(uint32_t v, uint32_t* part) {
+    v = __reduce_max_sync(0xffffffffu, v);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) v = max(v, part[w]);
+    return v;
+}
+
 template <int T>
 constexpr int kAppendThreads = T == 128 ? 512 : 256;
 
@@ -68,13 +81,13 @@ __global__ void __launch_bounds__(kAppendThreads<T>) cache_append_kernel(CacheVi
                                                                            const void* __restrict__ v_new,
                                                                            long long k_stride, long long v_stride,
                                                                            const int32_t* __restrict__ tok_ptr, int N,
-                                                                           int units, unsigned* err) {
+                                                                           int units, int groups, unsigned* err) {
     constexpr int NT = kAppendThreads<T>;
     constexpr int CH = T * kChunksPerToken / NT;  // chunks of one thread
     constexpr int W = BF16 ? 1 : 2;               // 16-byte words of a chunk
     __shared__ int s_req;
     __shared__ uint32_t s_max[2][NT / 32];
-    const int tid = threadIdx.x, item = blockIdx.x;
+    const int tid = threadIdx.x, item = blockIdx.x / groups;
     grid_dep_wait();
     if (tid == 0) s_req = -1;
     __syncthreads();
@@ -99,7 +112,7 @@ __global__ void __launch_bounds__(kAppendThreads<T>) cache_append_kernel(CacheVi
         return;
     }
     // units (K or V of a head) [u0, u1): the next one's tokens are on their way while one is written
-    const int u0 = blockIdx.y * units, u1 = min(2 * c.Hkv, u0 + units);
+    const int u0 = (blockIdx.x - item * groups) * units, u1 = min(2 * c.Hkv, u0 + units);
     const auto load = [&](int u, uint4 (&raw)[CH][W]) {
         const char* in = static_cast<const char*>((u & 1) ? v_new : k_new);
         const long long stride = (u & 1) ? v_stride : k_stride;
@@ -126,7 +139,7 @@ __global__ void __launch_bounds__(kAppendThreads<T>) cache_append_kernel(CacheVi
         const float s_old = a > 0 ? *scale : 0.f;
         if (u + 1 < u1) load(u + 1, next);
         uint8_t* out = (isv ? c.V : c.K) + ((size_t)phys * c.Hkv + h) * T * kHeadDim;
-        // the largest finite magnitude of the run's tokens
+        // the largest magnitude of the run's tokens; among finite ones only where one is not finite
         uint32_t amax = 0;
 #pragma unroll
         for (int x = 0; x < CH; ++x)
@@ -134,17 +147,29 @@ __global__ void __launch_bounds__(kAppendThreads<T>) cache_append_kernel(CacheVi
             for (int v = 0; v < W; ++v) {
                 const uint32_t w[4] = {raw[x][v].x, raw[x][v].y, raw[x][v].z, raw[x][v].w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t lo = BF16 ? (w[e] << 16) & 0x7fffffffu : w[e] & 0x7fffffffu, hi = w[e] & 0x7fff0000u;
-                    if (lo < 0x7f800000u) amax = max(amax, lo);
-                    if (BF16 && hi < 0x7f800000u) amax = max(amax, hi);
-                }
+                for (int e = 0; e < 4; ++e)  // bf16: both halves at once
+                    amax = BF16 ? __vmaxu2(amax, w[e] & 0x7fff7fffu) : max(amax, w[e] & 0x7fffffffu);
             }
-        amax = __reduce_max_sync(0xffffffffu, amax);
-        if ((tid & 31) == 0) s_max[u & 1][tid >> 5] = amax;
-        __syncthreads();
+        if (BF16) amax = max(amax << 16, amax & 0xffff0000u);
+        amax = cta_max<NT / 32>(amax, s_max[u & 1]);
+        const bool finite = amax < 0x7f800000u;
+        if (!finite) {
+            uint32_t top = 0;
 #pragma unroll
-        for (int w = 0; w < NT / 32; ++w) amax = max(amax, s_max[u & 1][w]);
+            for (int x = 0; x < CH; ++x)
+#pragma unroll
+                for (int v = 0; v < W; ++v) {
+                    const uint32_t w[4] = {raw[x][v].x, raw[x][v].y, raw[x][v].z, raw[x][v].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t lo = BF16 ? (w[e] << 16) & 0x7fffffffu : w[e] & 0x7fffffffu, hi = w[e] & 0x7fff0000u;
+                        if (lo < 0x7f800000u) top = max(top, lo);
+                        if (BF16 && hi < 0x7f800000u) top = max(top, hi);
+                    }
+                }
+            __syncthreads();  // every thread has read the first maximum
+            amax = cta_max<NT / 32>(top, s_max[u & 1]);
+        }
         if (!(s_old >= 0.f) || (__float_as_uint(s_old) & 0x7f800000u) == 0x7f800000u) {
             if (tid == 0) atomicOr(err, QUP_ERR_SCALE);
         } else {
@@ -152,6 +177,7 @@ __global__ void __launch_bounds__(kAppendThreads<T>) cache_append_kernel(CacheVi
             // 1 / s is exact for a power of two; a caller's own scale (s_old kept) takes the division
             const bool exact = (__float_as_uint(s) & 0x7fffffu) == 0 && s < 8.5e37f;  // 2^126
             const float inv = exact ? pow2(127 - (int)(__float_as_uint(s) >> 23)) : 0.f;
+            const bool plain = finite && exact;
 #pragma unroll
             for (int x = 0; x < CH; ++x) {
                 const int at = tid + x * NT, slot = at / kChunksPerToken, part = at % kChunksPerToken;
@@ -167,6 +193,7 @@ __global__ void __launch_bounds__(kAppendThreads<T>) cache_append_kernel(CacheVi
                         f[2 * e] = f16_lo(v) * ratio;
                         f[2 * e + 1] = f16_hi(v) * ratio;
                     }
+                    *dst = make_uint2(pack_e4m3_checked(f), pack_e4m3_checked(f + 4));
                 } else if (slot < b) {
                     if constexpr (BF16) {
                         const uint32_t w[4] = {raw[x][0].x, raw[x][0].y, raw[x][0].z, raw[x][0].w};
@@ -184,12 +211,16 @@ __global__ void __launch_bounds__(kAppendThreads<T>) cache_append_kernel(CacheVi
                             f[4 * v + 3] = __uint_as_float(raw[x][v].w);
                         }
                     }
+                    if (plain) {
 #pragma unroll
-                    for (int e = 0; e < kChunk; ++e) f[e] = exact ? f[e] * inv : __fdiv_rn(f[e], s);
-                } else {
-                    continue;
+                        for (int e = 0; e < kChunk; ++e) f[e] *= inv;
+                        *dst = make_uint2(pack_e4m3x4(f[0], f[1], f[2], f[3]), pack_e4m3x4(f[4], f[5], f[6], f[7]));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < kChunk; ++e) f[e] = exact ? f[e] * inv : __fdiv_rn(f[e], s);
+                        *dst = make_uint2(pack_e4m3_checked(f), pack_e4m3_checked(f + 4));
+                    }
                 }
-                *dst = make_uint2(pack_e4m3_checked(f), pack_e4m3_checked(f + 4));
             }
             if (tid == 0 && (a == 0 || s != s_old)) *scale = s;
         }
@@ -208,11 +239,13 @@ cudaError_t launch_t(const CacheView& c, const void* k_new, const void* v_new, b
     // there are CTAs enough to fill the SMs several times
     const int all = 2 * c.Hkv;
     const int units = (int)std::max<long long>(1, std::min<long long>(std::min(8, all), items * all / (16ll * sms)));
-    const dim3 grid((unsigned)items, (unsigned)((all + units - 1) / units)), block(kAppendThreads<T>);
+    // a run's units are neighbours in the grid: they read the same tokens' rows at about the same time
+    const int groups = (all + units - 1) / units;
+    const dim3 grid((unsigned)(items * groups)), block(kAppendThreads<T>);
     return bf16 ? launch_pdl(cache_append_kernel<T, true>, grid, block, 0, stream, c, k_new, v_new, k_stride, v_stride,
-                             tok_ptr, N, units, err)
+                             tok_ptr, N, units, groups, err)
                 : launch_pdl(cache_append_kernel<T, false>, grid, block, 0, stream, c, k_new, v_new, k_stride, v_stride,
-                             tok_ptr, N, units, err);
+                             tok_ptr, N, units, groups, err);
 }
 
 }  // namespace

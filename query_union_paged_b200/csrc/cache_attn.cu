@@ -857,6 +857,44 @@ __device__ __forceinline__ void merge_write(const CacheAttnParams& p, int q0, in
     }
 }
 
+// Row x of query q0's tile from nc partial results, at(c) their places: 32 maxima and sums at a time, a lane
+// each, and the outputs added in order.
+template <class At>
+__device__ __forceinline__ void merge_row(const CacheAttnParams& p, int q0, int h, int x, int nc, int lane, At at) {
+    float M = kNegInf, Ls = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int b = 0; b < nc; b += 32) {
+        float2 ml = make_float2(kNegInf, 0.f);
+        if (b + lane < nc) ml = p.part_ml[at(b + lane)];
+        float top = ml.x;
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+        if (top > M) {  // what was added so far is relative to M
+            const float f = ex2(M - top);
+            Ls *= f;
+            acc.x *= f;
+            acc.y *= f;
+            acc.z *= f;
+            acc.w *= f;
+            M = top;
+        }
+        // a part that saw nothing holds zeros; NaN goes through
+        const float f = ml.x == kNegInf ? (ml.y == 0.f ? 0.f : 1.f) : ex2(ml.x - M);
+        const float lf = ml.y * f;
+#pragma unroll 4
+        for (int c = 0; c < min(32, nc - b); ++c) {
+            const float fc = __shfl_sync(0xffffffffu, f, c);
+            const float4 v = reinterpret_cast<const float4*>(p.part_o + at(b + c) * kHeadDim)[lane];
+            Ls += __shfl_sync(0xffffffffu, lf, c);
+            acc.x += v.x * fc;
+            acc.y += v.y * fc;
+            acc.z += v.z * fc;
+            acc.w += v.w * fc;
+        }
+    }
+    merge_write(p, q0, h, x, M, Ls, acc, lane);
+}
+
 // One CTA per item: the partial results of its rows, in the order of the CTAs that left them.  Rows
 // of an item that one CTA finished are left alone; rows that see nothing get O = 0, lse = -inf.
 template <int RT, bool SPARSE>
@@ -924,45 +962,15 @@ __global__ void __launch_bounds__(kHeadDim) cache_merge_kernel(const __grid_cons
             nc = (int)((a + nvis - 1) / per) - c0 + 1;
             if (nc == 1) return;
             // CTA c's partial is its first segment's unless the item begins inside its run
-            row0 = tile * RT;
-            for (int rr = warp; rr < rows; rr += kHeadDim / 32) {
-                float M = kNegInf, Ls = 0.f;
-                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int c = c0; c < c0 + nc; ++c)
-                    M = fmaxf(M, p.part_ml[((size_t)2 * c + ((long long)c * per >= a ? 0 : 1)) * RT + rr].x);
-                for (int c = c0; c < c0 + nc; ++c) {
-                    const size_t at = ((size_t)2 * c + ((long long)c * per >= a ? 0 : 1)) * RT + rr;
-                    const float2 ml = p.part_ml[at];
-                    const float f = ml.x == kNegInf ? (ml.y == 0.f ? 0.f : 1.f) : ex2(ml.x - M);
-                    const float4 v = reinterpret_cast<const float4*>(p.part_o + at * kHeadDim)[lane];
-                    Ls += ml.y * f;
-                    acc.x += v.x * f;
-                    acc.y += v.y * f;
-                    acc.z += v.z * f;
-                    acc.w += v.w * f;
-                }
-                merge_write(p, q0, h, row0 + rr, M, Ls, acc, lane);
-            }
+            for (int rr = warp; rr < rows; rr += kHeadDim / 32)
+                merge_row(p, q0, h, row0 + rr, nc, lane, [&](int c) {
+                    return ((size_t)2 * (c0 + c) + ((long long)(c0 + c) * per >= a ? 0 : 1)) * RT + rr;
+                });
             return;
         }
     }
-    for (int rr = warp; rr < rows; rr += kHeadDim / 32) {
-        float M = kNegInf, Ls = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int c = c0; c < c0 + nc; ++c) M = fmaxf(M, p.part_ml[(size_t)c * RT + rr].x);
-        for (int c = c0; c < c0 + nc; ++c) {
-            const size_t at = (size_t)c * RT + rr;
-            const float2 ml = p.part_ml[at];
-            const float f = ml.x == kNegInf ? (ml.y == 0.f ? 0.f : 1.f) : ex2(ml.x - M);
-            const float4 v = reinterpret_cast<const float4*>(p.part_o + at * kHeadDim)[lane];
-            Ls += ml.y * f;
-            acc.x += v.x * f;
-            acc.y += v.y * f;
-            acc.z += v.z * f;
-            acc.w += v.w * f;
-        }
-        merge_write(p, q0, h, row0 + rr, M, Ls, acc, lane);
-    }
+    for (int rr = warp; rr < rows; rr += kHeadDim / 32)
+        merge_row(p, q0, h, row0 + rr, nc, lane, [&](int c) { return (size_t)(c0 + c) * RT + rr; });
 }
 
 // ------------------------------------------------------------------ page weights
