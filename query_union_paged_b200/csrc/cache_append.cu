@@ -12,7 +12,8 @@
 // reduced over the CTA, and the registers are scaled, rounded (nearest even) and written; the next
 // unit's loads are under way meanwhile.  A run without infinities and NaN takes the short way: two
 // magnitudes an instruction, no test of each value (with them the kernel was bound by its instructions,
-// 3.4 TB/s).  Bound by DRAM: N * Hkv * 128 * (element + 1) bytes for each of
+// 3.4 TB/s; now 5.3 TB/s for 83K tokens of 8 heads, and 7 us where 64 requests write one token each: a
+// launch and four dependent loads).  Bound by DRAM: N * Hkv * 128 * (element + 1) bytes for each of
 // K and V.
 #include <algorithm>
 #include <cstdint>

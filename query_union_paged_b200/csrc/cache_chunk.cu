@@ -25,7 +25,14 @@
 // NaN: a NaN byte of V that a row does not see must not reach it as 0 * NaN.  The converters store 0 for
 // it and remember its column's first such token; the epilogue gives NaN to the rows that see it.
 //
-// Bound by the tensor cores and the exponentials: 4 * rows * tokens * 128 flops.
+// Bound: a step of 256 rows takes about 4,600 cycles.  The two warpgroups' softmax takes 2,500 to 3,200 of
+// them together (their exponentials alone 1,800 to 2,100, of which the MUFU unit 1,540), the tensor
+// cores 2,050; what does not overlap is the way from P to the next S (O update, S, two completions of
+// 200 to 400 cycles each).  1,024 queries x 32 heads behind 16K tokens: 335 us, 0.85 PFLOP/s.
+// Measured and left out: loops unrolled over a step (instruction fetch: +23 %), the warpgroups taking
+// turns (+57 %: one alone is hardly faster than both together), half steps with S, P and O update of their
+// own (+14 %: products of 64 columns take as long to issue as of 128), four converting warps of 128
+// registers (+3 %), an E4M3 pair for P as for Q (three conversions of 6 cycles a pair instead of one of 2).
 #include <algorithm>
 #include <cstdint>
 
@@ -50,7 +57,7 @@ constexpr int kMarks = 5;                   // segments whose NaN marks are held
 constexpr int kMaxPages = kStep / 16;
 constexpr int kMmaWarp = 8, kLoadWarp = 9, kConvWarp = 10, kConvWarps = 2;
 constexpr uint32_t kColO = 0, kColS = 256;
-constexpr int kPolyPairs = 3;      // of every eight pairs of exponentials, those on the FMA pipe
+constexpr int kPolyPairs = 2;      // of every eight pairs of exponentials, those on the FMA pipe
 constexpr float kOffset = 8.f;     // log2 offset of P
 constexpr float kLazy = 7.f;       // the maximum moves once a score passes it by this: P <= 2^15
 constexpr float kZeroScaleLog2 = -64.f;
@@ -395,64 +402,64 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float ks = 0.f, vl = 0.f, vi = 0.f;
                 for (int b = sg.b0; b < b1 && ok; ++b, ++it) {
                     const int pe = b * PPS;
-                if (pe + PPS > have1) {
-                    have0 = pe;
-                    have1 = pe + 32;
-                    const int e = pe + lane;
-                    phys = -1;
-                    if (e < last) {
-                        phys = p.c.page_table[p0 + e];
-                        if (phys < 0 || phys >= p.c.P_phys) {
-                            atomicOr(p.err, QUP_ERR_PHYS_PAGE);
-                            phys = -1;
-                        } else {
-                            ks = __ldg(p.c.k_scale + (size_t)phys * p.c.Hkv + h);
-                            const float vs = __ldg(p.c.v_scale + (size_t)phys * p.c.Hkv + h);
-                            if (!(fabsf(ks) < INFINITY) || !(vs >= 0.f && vs < INFINITY)) {
-                                atomicOr(p.err, QUP_ERR_SCALE);
+                    if (pe + PPS > have1) {
+                        have0 = pe;
+                        have1 = pe + 32;
+                        const int e = pe + lane;
+                        phys = -1;
+                        if (e < last) {
+                            phys = p.c.page_table[p0 + e];
+                            if (phys < 0 || phys >= p.c.P_phys) {
+                                atomicOr(p.err, QUP_ERR_PHYS_PAGE);
                                 phys = -1;
+                            } else {
+                                ks = __ldg(p.c.k_scale + (size_t)phys * p.c.Hkv + h);
+                                const float vs = __ldg(p.c.v_scale + (size_t)phys * p.c.Hkv + h);
+                                if (!(fabsf(ks) < INFINITY) || !(vs >= 0.f && vs < INFINITY)) {
+                                    atomicOr(p.err, QUP_ERR_SCALE);
+                                    phys = -1;
+                                }
+                                vl = vs > 0.f ? lg2(vs) : kZeroScaleLog2;
+                                vi = vs > 0.f ? __frcp_rn(vs) : 18446744073709551616.f;
                             }
-                            vl = vs > 0.f ? lg2(vs) : kZeroScaleLog2;
-                            vi = vs > 0.f ? __frcp_rn(vs) : 18446744073709551616.f;
                         }
+                        if (phys < 0) ks = vl = vi = 0.f;
                     }
-                    if (phys < 0) ks = vl = vi = 0.f;
-                }
-                const int src = pe - have0;
-                const uint32_t live = (__ballot_sync(0xffffffffu, phys >= 0) >> src) & ((1u << PPS) - 1u);
-                const uint32_t neg = (__ballot_sync(0xffffffffu, ks < 0.f) >> src) & ((1u << PPS) - 1u);
-                const uint32_t bytes = __popc(live) * T * kHeadDim;
+                    const int src = pe - have0;
+                    const uint32_t live = (__ballot_sync(0xffffffffu, phys >= 0) >> src) & ((1u << PPS) - 1u);
+                    const uint32_t neg = (__ballot_sync(0xffffffffu, ks < 0.f) >> src) & ((1u << PPS) - 1u);
+                    const uint32_t bytes = __popc(live) * T * kHeadDim;
 #pragma unroll
-                for (int kv = 0; kv < 2; ++kv) {
-                    const int n = kv ? kNV : kNK;
-                    const uint32_t slot = it % n, par = (it / n) & 1;
-                    if (!warp_ok(mbar_wait_idle(kv ? B.vempty(slot) : B.kempty(slot), par ^ 1, abort_flag, p.err,
-                                                QUP_ERR_TIMEOUT, lim)))
-                        ok = false;
-                    if (!ok) break;
-                    if (kv == 0) {
-                        // the constants' last readers, kNM steps ago, are done: S of a later step has run
-                        StepMeta& m = meta[it % kNM];
-                        if (lane >= src && lane < src + PPS) m.page[lane - src] = make_float4(ks, vl, vi, 0.f);
+                    for (int kv = 0; kv < 2; ++kv) {
+                        const int n = kv ? kNV : kNK;
+                        const uint32_t slot = it % n, par = (it / n) & 1;
+                        if (!warp_ok(mbar_wait_idle(kv ? B.vempty(slot) : B.kempty(slot), par ^ 1, abort_flag, p.err,
+                                                    QUP_ERR_TIMEOUT, lim)))
+                            ok = false;
+                        if (!ok) break;
+                        if (kv == 0) {
+                            // the constants' last readers, kNM steps ago, are done: S of a later step has run
+                            StepMeta& m = meta[it % kNM];
+                            if (lane >= src && lane < src + PPS) m.page[lane - src] = make_float4(ks, vl, vi, 0.f);
+                            if (lane == 0) {
+                                m.valid = live;
+                                m.negative = neg;
+                            }
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(B.mfull(it % kNM));
+                        }
+                        const uint32_t full = kv ? B.vfull(slot) : B.kfull(slot);
                         if (lane == 0) {
-                            m.valid = live;
-                            m.negative = neg;
+                            if (bytes) mbar_arrive_expect_tx(full, bytes);
+                            else mbar_arrive(full);
                         }
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(B.mfull(it % kNM));
+                        if (lane >= src && lane < src + PPS && phys >= 0)
+                            tma_load_4d(sbase + (kv ? Layout::v : Layout::k) + slot * kTile +
+                                            (uint32_t)(lane - src) * T * kHeadDim,
+                                        kv ? &tmV : &tmK, full, 0, 0, h, phys);
+                        __syncwarp();
                     }
-                    const uint32_t full = kv ? B.vfull(slot) : B.kfull(slot);
-                    if (lane == 0) {
-                        if (bytes) mbar_arrive_expect_tx(full, bytes);
-                        else mbar_arrive(full);
-                    }
-                    __syncwarp();
-                    if (lane >= src && lane < src + PPS && phys >= 0)
-                        tma_load_4d(sbase + (kv ? Layout::v : Layout::k) + slot * kTile +
-                                        (uint32_t)(lane - src) * T * kHeadDim,
-                                    kv ? &tmV : &tmK, full, 0, 0, h, phys);
-                    __syncwarp();
-                }
                 }
             }
             if (lane == 0) {

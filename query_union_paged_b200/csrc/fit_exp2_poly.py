@@ -1,4 +1,4 @@
-"""Fit the cubic used by exp2_poly2 (ptx.cuh): p(f) = 1 + f (c1 + f (c2 + f c3)) ~ 2^f on
+"""Fit the cubic used by exp2_poly2 and the quartic of exp2_poly2q (ptx.cuh): p(f) = 1 + f (c1 + f (c2 + f c3)) ~ 2^f on
 [-1/2, 1/2], minimising the maximum relative error |p(f) / 2^f - 1| as a linear program over a
 dense grid, then reporting the error of the fp32-rounded coefficients evaluated in fp32 the
 way the kernel does (Horner with fused multiply-adds).
@@ -37,4 +37,7 @@ def fp32_error(coef, n=200001):
 if __name__ == "__main__":
     coef, err = fit()
     print("c1..c3 =", ", ".join(f"{np.float32(c)!r}" for c in coef))
+    print(f"LP max relative error {err:.3e}; fp32 evaluation {fp32_error(coef):.3e}")
+    coef, err = fit(4)  # exp2_poly2q
+    print("q1..q4 =", ", ".join(f"{np.float32(c)!r}" for c in coef))
     print(f"LP max relative error {err:.3e}; fp32 evaluation {fp32_error(coef):.3e}")

@@ -470,7 +470,7 @@ __device__ __forceinline__ f2 exp2_poly2(f2 y) {
 
 // exp2_poly2 with a quartic (the same fit: max relative error 2.8e-6, below fp16's half step of 2^-11
 // by 170, so that a sum of many keeps it).
-constexpr float kExp2Q1 = 0.6931242f, kExp2Q2 = 0.24024099f, kExp2Q3 = 0.055906426f, kExp2Q4 = 0.009582853f;
+constexpr float kExp2Q1 = 0.693124f, kExp2Q2 = 0.24024066f, kExp2Q3 = 0.05590752f, kExp2Q4 = 0.009584325f;
 __device__ __forceinline__ f2 exp2_poly2q(f2 y) {
     const f2 kMagic{12582912.f, 12582912.f};
     y.x = fmaxf(y.x, -127.f);

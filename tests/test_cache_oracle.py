@@ -158,3 +158,23 @@ def test_python_refusals():
             qup.KVCache(**{**good, **bad})
     with pytest.raises(ValueError, match="CUDA"):
         qup.KVCache(**good)
+
+
+def test_quartic_exponential_is_the_fit_and_within_its_bound():
+    import importlib.util
+    import os
+    import re
+
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "query_union_paged_b200", "csrc")
+    m = re.search(r"kExp2Q1 = ([0-9.]+)f, kExp2Q2 = ([0-9.]+)f, kExp2Q3 = ([0-9.]+)f, kExp2Q4 = ([0-9.]+)f",
+                  open(os.path.join(csrc, "ptx.cuh")).read())
+    have = [np.float32(x) for x in m.groups()]
+    spec = importlib.util.spec_from_file_location("fit_exp2_poly", os.path.join(csrc, "fit_exp2_poly.py"))
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    coef, err = mod.fit(4)
+    # coefficients of a nearly flat optimum move by more than their effect: compare what they evaluate to
+    f = np.linspace(-0.5, 0.5, 20001)
+    poly = lambda c: 1 + f * (c[0] + f * (c[1] + f * (c[2] + f * c[3])))
+    assert np.abs(poly([float(x) for x in have]) / poly(coef) - 1).max() < 2e-7
+    assert err < 2.9e-6 and mod.fp32_error(have) < 3.1e-6  # fp32 evaluation adds at most 3 steps of 2^-24

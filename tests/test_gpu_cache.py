@@ -516,6 +516,56 @@ def test_same_bits_every_run_on_two_streams_at_once_and_in_graphs():
     assert all(torch.equal(a, b) for a, b in zip(want, outs)) and qup.get_error() == 0
 
 
+def test_a_step_of_all_calls_in_one_graph_and_chunks_on_two_streams():
+    """Append, chunk attention with page weights and eviction captured together and replayed on changed
+    contents; two chunk calls at the same time give the bits of one alone."""
+    torch = _t()
+    c = Case(62, [300, 150, 220], T=32, Hkv=2, fill_tail=None)
+    ns, g = [70, 30, 3], 4
+    ptr = torch.from_numpy(_ptr(ns)).cuda()
+    cache, ref = c.cache(), c.cache()
+    N = sum(ns)
+    k, v = (torch.empty(N, 2, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q = torch.empty(N, 8, 128, dtype=torch.bfloat16, device="cuda")
+    n = len(c.table)
+
+    def step(cache, o, w, acc, out, ws):
+        qup.cache_append(cache, k, v, ptr)
+        qup.cache_attn(cache, q, ptr, 70, out=o, page_weight=w, workspace=ws)
+        qup.cache_evict(cache, w, acc, 4, decay=0.5, out=out)
+
+    def buffers(cache):
+        return (torch.empty_like(q), torch.empty(n, 2, device="cuda"), torch.zeros(n, device="cuda"),
+                (torch.empty_like(cache.page_table), torch.empty(n, device="cuda"), torch.empty_like(cache.kv_len),
+                 torch.empty_like(cache.page_table)), qup.cache_attn_workspace(cache, N, 8, 70, page_weight=True))
+
+    gen = torch.Generator("cuda").manual_seed(5)
+    fill = lambda: [t.copy_(torch.randn(t.shape, generator=gen, device="cuda")) for t in (k, v, q)]
+    fill()
+    a, b = buffers(cache), buffers(ref)
+    step(cache, *a)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(cache, *a)
+    for _ in range(2):
+        fill()
+        cache.K.copy_(ref.K), cache.V.copy_(ref.V), cache.k_scale.copy_(ref.k_scale), cache.v_scale.copy_(ref.v_scale)
+        graph.replay()
+        step(ref, *b)
+        torch.cuda.synchronize()
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and all(torch.equal(x, y) for x, y in zip(a[3], b[3]))
+    streams, outs = [torch.cuda.Stream() for _ in range(2)], [torch.empty_like(q) for _ in range(2)]
+    ws = [qup.cache_attn_workspace(ref, N, 8, 70) for _ in range(2)]
+    want = qup.cache_attn(ref, q, ptr, 70)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, o, x in zip(streams, outs, ws):
+            qup.cache_attn(ref, q, ptr, 70, out=o, workspace=x, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs) and qup.get_error() == 0
+
+
 # ------------------------------------------------------------------ eviction
 
 @pytest.mark.parametrize("budget,sink,recent,decay", [(5, 1, 2, 0.9), (1, 0, 1, 1.0), (3, 4, 4, 0.0), (100, 1, 1, 0.5),
