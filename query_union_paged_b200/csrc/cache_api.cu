@@ -161,8 +161,10 @@ int qup_cache_attn(const qup_cache* cache, const void* Q, int64_t q_stride, cons
     p.big_rows = !chunk ? 0x7fffffff : (small ? qup::kCacheSmallRows + 1 : 1);
     p.max_tiles = (int)((small_rows + rt - 1) / rt);
     const int64_t max_units = ((int64_t)c.max_pages * c.T + qup::kCacheUnit - 1) / qup::kCacheUnit;
-    // the chunk kernel counts steps in 32 bits
-    if (chunk && ((int64_t)c.max_pages * c.T + 256 + max_q) * g + 256 >= ((int64_t)1 << 31)) return QUP_ERR_ARG;
+    // the chunk kernel counts steps and a request's rows in 32 bits
+    if (chunk && (((int64_t)c.max_pages * c.T + 256 + max_q) * g + 256 >= ((int64_t)1 << 31) ||
+                  (int64_t)max_q * Hq >= ((int64_t)1 << 31)))
+        return QUP_ERR_ARG;
     if (!sparse && (int64_t)p.max_tiles * c.Hkv * max_units >= ((int64_t)1 << 31)) return QUP_ERR_ARG;
     const int64_t items = sparse ? (int64_t)Nq * c.Hkv : (int64_t)c.R * c.Hkv * p.max_tiles;
     if (items >= ((int64_t)1 << 31) / 2) return QUP_ERR_ARG;

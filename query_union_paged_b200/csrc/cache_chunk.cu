@@ -655,25 +655,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int vis = wk.it.ok ? wk.it.q.len - wk.it.q.n + qi + 1 : 0;
             const int vis_all = wk.it.ok ? wk.it.q.len - wk.it.q.n + row0 / g + 1 : 0;
             // ---- Q: high and low E4M3 parts of the warp's rows, each row's score factor.  16 lanes share a
-            // row: 8 elements each.
+            // row: 8 elements each.  The bf16 rows come into the places that their two parts will take.
             float rs = 0.f;
             {
                 const uint16_t* q0 = static_cast<const uint16_t*>(p.Q) + (size_t)wk.it.q.q0 * p.q_stride +
                                      (size_t)(sg.h * g) * kHeadDim + (lane & 15) * 8;
-                uint8_t* qt = smem + Layout::q + w * 2 * kTile + (wq * 32 + (lane >> 4)) * 128;
-#pragma unroll 1
-                for (int i0 = 0; i0 < 16; i0 += 8) {
-                uint4 raw[8];
-#pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    const int i = i0 + u;
-                    const int y = row0 + min(wq * 32 + 2 * i + (lane >> 4), rows - 1), yq = y / g;
-                    raw[u] = __ldg(reinterpret_cast<const uint4*>(q0 + (size_t)yq * p.q_stride + (y - yq * g) * kHeadDim));
+                uint8_t* qt = smem + Layout::q + w * 2 * kTile + wq * 32 * 128;
+                const uint32_t from = (uint32_t)((lane & 8) ? kTile : 0) + (lane >> 4) * 128 + (lane & 7) * 16;
+#pragma unroll 4
+                for (int i = 0; i < 16; ++i) {
+                    const int row = 2 * i + (lane >> 4);
+                    const int yq = __shfl_sync(0xffffffffu, qi, row), yj = __shfl_sync(0xffffffffu, j, row);
+                    copy16_async(smem_u32(qt) + from + i * 256, q0 + (size_t)yq * p.q_stride + yj * kHeadDim);
                 }
-#pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    const int i = i0 + u;
-                    const uint32_t w4[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+                copy_async_wait();
+                __syncwarp();
+#pragma unroll 1
+                for (int i = 0; i < 16; ++i) {
+                    const uint4 raw = *reinterpret_cast<const uint4*>(qt + from + i * 256);
+                    const uint32_t w4[4] = {raw.x, raw.y, raw.z, raw.w};
                     uint32_t top = 0;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) top = max(top, max((w4[e] << 16) & 0x7f800000u, w4[e] & 0x7f800000u));
@@ -698,11 +698,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         f16x2_to_f32(cvt_e4m3x2(hi[e] >> 16), z[2], z[3]);
                         lo[e] = pack_e4m3x4(y[0] - z[0], y[1] - z[1], y[2] - z[2], y[3] - z[3]);
                     }
-                    const int row7 = (2 * i + (lane >> 4)) & 7, ch = (lane & 15) >> 1;
-                    uint8_t* dst = qt + i * 256 + ((ch ^ row7) << 4) + (lane & 1) * 8;
+                    __syncwarp();  // both rows have been read
+                    const int row = 2 * i + (lane >> 4), ch = (lane & 15) >> 1;
+                    uint8_t* dst = qt + row * 128 + ((ch ^ (row & 7)) << 4) + (lane & 1) * 8;
                     *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
                     *reinterpret_cast<uint2*>(dst + kTile) = make_uint2(lo[0], lo[1]);
-                }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -895,51 +895,39 @@ __global__ void __launch_bounds__(kThreads, 1)
             // 32 columns at a time through the warp's rows of the Q tile (every S that reads them is done),
             // so that a row's 128 (partial results) or 64 bytes leave as one piece
             uint8_t* stage = smem + Layout::q + w * 2 * kTile + wq * 32 * 128;
+            const float times = complete ? inv : 1.f;
+            const int place = qi * p.Hq + j;  // of the row in the request's output
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
                 uint32_t ov[32];
                 tmem_ld32_wait(o_addr + 32u * c, ov);
-                if (nan) {
+                __syncwarp();  // the columns before these have left
 #pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    *reinterpret_cast<float4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+                        make_float4(__uint_as_float(ov[4 * e]) * times, __uint_as_float(ov[4 * e + 1]) * times,
+                                    __uint_as_float(ov[4 * e + 2]) * times, __uint_as_float(ov[4 * e + 3]) * times);
+                if (nan) {
+#pragma unroll 1
                     for (int e = 0; e < 32; ++e)
-                        if (nm.first[32 * c + e] < vis) ov[e] = 0x7fc00000u;
+                        if (nm.first[32 * c + e] < vis)
+                            *reinterpret_cast<uint32_t*>(stage + lane * 128 + (((e >> 2) ^ (lane & 7)) << 4) + (e & 3) * 4) =
+                                0x7fc00000u;
                 }
                 __syncwarp();
-                if (complete) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t o[4];
-#pragma unroll
-                        for (int y = 0; y < 4; ++y)
-                            o[y] = pack_bf16x2(__uint_as_float(ov[8 * e + 2 * y]) * inv,
-                                               __uint_as_float(ov[8 * e + 2 * y + 1]) * inv);
-                        *reinterpret_cast<uint4*>(stage + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4)) =
-                            make_uint4(o[0], o[1], o[2], o[3]);
-                    }
-                    __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {  // 8 rows, 4 lanes each
-                        const int rr = 8 * i + (lane >> 2);
-                        const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4));
-                        if (wq * 32 + rr < rows) {
-                            const int y = row0 + wq * 32 + rr, yq = y / g;
-                            const size_t to = (q0 + yq) * p.Hq + sg.h * g + (y - yq * g);
-                            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.O) + to * kHeadDim + 32 * c + (lane & 3) * 8) = v;
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        *reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
-                            make_uint4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
-                    __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {  // 4 rows, 8 lanes each
-                        const int rr = 4 * i + (lane >> 3);
-                        const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
-                        if (wq * 32 + rr < rows)
-                            *reinterpret_cast<uint4*>(p.chunk_o + (prow0 + rr) * kHeadDim + 32 * c + (lane & 7) * 4) = v;
-                    }
+#pragma unroll 2
+                for (int i = 0; i < 8; ++i) {  // 4 rows, 8 lanes each
+                    const int rr = 4 * i + (lane >> 3);
+                    const float4 v = *reinterpret_cast<const float4*>(stage + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
+                    const int to = __shfl_sync(0xffffffffu, place, rr);
+                    if (wq * 32 + rr >= rows) continue;
+                    const int col = 32 * c + (lane & 7) * 4;
+                    if (complete)
+                        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.O) +
+                                                  (q0 * p.Hq + sg.h * g + (size_t)to) * kHeadDim + col) =
+                            make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+                    else
+                        *reinterpret_cast<float4*>(p.chunk_o + (prow0 + rr) * kHeadDim + col) = v;
                 }
             }
             __syncwarp();
