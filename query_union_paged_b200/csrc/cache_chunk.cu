@@ -31,7 +31,8 @@
 // 200 to 400 cycles each).  1,024 queries x 32 heads behind 16K tokens: 335 us, 0.85 PFLOP/s.
 // Measured and left out: loops unrolled over a step (instruction fetch: +23 %), the warpgroups taking
 // turns (+57 %: one alone is hardly faster than both together), half steps with S, P and O update of their
-// own (+14 %: products of 64 columns take as long to issue as of 128), four converting warps of 128
+// own (+14 %: products of 64 columns take as long to issue as of 128), a step's tokens split over both
+// warpgroups for items of few rows (-6 % for 35 rows, +3 % for chunks), four converting warps of 128
 // registers (+3 %), an E4M3 pair for P as for Q (three conversions of 6 cycles a pair instead of one of 2).
 #include <algorithm>
 #include <cstdint>
@@ -670,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 copy_async_wait();
                 __syncwarp();
-#pragma unroll 1
+#pragma unroll 2
                 for (int i = 0; i < 16; ++i) {
                     const uint4 raw = *reinterpret_cast<const uint4*>(qt + from + i * 256);
                     const uint32_t w4[4] = {raw.x, raw.y, raw.z, raw.w};

@@ -12,7 +12,11 @@ Attention bounds (per element, E = 2^-24 the fp32 half step):
           where that is coarser than its last bit, so |ds| grows by 2^-17 max|q| sum|k|, which is at most
           2^-17 * (sum|q||k| max|q| sum|k| / sum|q||k|); the oracle returns qk = max|q| sum|k| (scaled)
   lse     |ds| + 2^-18 + E |lse| + E * tokens (the sum of weights, in order)
-  page weights  a relative 2 |ds| + 2^-17 + 2 E * tokens
+  page weights  a relative 2 |ds| + 2^-17 + 2 E * tokens, and what is flushed: a token's exponential is
+          p = 2^(x - m + 8), x = log2(e) s + log2 vs (a scale of 0 counts as 2^-64), and lost below 2^-126.  Its
+          weight is p / vs * 2^(m - 8 - lse'), with lse' the row's lse in base 2.  m is at most the largest x,
+          so at most lse' + log2 of the head's largest scale: a token loses less than
+          2^-134 vs_max / vs, a page that for each of its tokens and the request's rows
 """
 import math
 
@@ -99,7 +103,7 @@ def _check_attn(got, lse, weight, ref, tokens, what, p_round=2.0 ** -11):
         le = np.abs(np.where(fin, lse, 0) - np.where(fin, ref["lse"], 0))
         assert np.all(le <= lt), (what, float((le - lt).max()))
     if weight is not None:
-        wt = ref["weight"] * (2 * ds.max() + 2.0 ** -17 + 2 * E * tokens) + 1e-30
+        wt = ref["weight"] * (2 * ds.max() + 2.0 ** -17 + 2 * E * tokens) + ref.get("flushed", 0.0) + 1e-30
         we = np.abs(weight - ref["weight"])
         assert np.all(we <= wt), (what, float((we - wt).max()))
 
@@ -123,6 +127,8 @@ def _run_attn(c, ns, g, topk=None, weights=True, scale=None, qstd=1.5, max_q=Non
     torch.cuda.synchronize()
     assert qup.get_error() == 0
     ref = oc.attn(qv, c.K, c.V, c.ks, c.vs, c.table, c.page_ptr, c.lens, ptr, scale, topk)
+    vs = np.maximum(np.abs(c.vs[c.table].astype(np.float64)), 2.0 ** -64)
+    ref["flushed"] = 2.0 ** -134 * c.T * max(ns) * g * vs.max(axis=0) / vs
     return (o.double().cpu().numpy(), lse.double().cpu().numpy(), None if w is None else w.double().cpu().numpy(), ref)
 
 
@@ -282,6 +288,19 @@ def test_peaked_and_flat_softmax(qstd, scale):
     c = Case(14, [513, 64], T=64, spread=6.0)
     o, lse, w, ref = _run_attn(c, [3, 1], 4, qstd=qstd, scale=scale)
     _check_attn(o, lse, w, ref, 513, (qstd, scale))
+
+
+@pytest.mark.parametrize("T", [16, 64, 128])
+@pytest.mark.parametrize("g,n", [(8, 5), (8, 20), (8, 40)])
+def test_rows_of_every_width_peaked_and_with_odd_scales(T, g, n):
+    """40, 160 and 320 rows: one row tile split over both warpgroups (pages of up to 64), one, and two."""
+    c = Case(T + n, [700, 129 + n, n + 3], T=T, spread=6.0)
+    p = c.table[:c.page_ptr[1]]
+    c.vs[p[1]], c.V[p[1]], c.ks[p[2]] = 0.0, 0, 0.0
+    c.ks[p[3]] = -c.ks[p[3]]
+    c.vs[p[4]] *= 1.37 * 2.0 ** 12
+    o, lse, w, ref = _run_attn(c, [n, n, n], g, qstd=12.0)
+    _check_attn(o, lse, w, ref, 700, (T, g, n))
 
 
 def test_pages_of_zero_scale_and_of_far_apart_scales():
