@@ -63,10 +63,11 @@ struct PageMeta {
     int pad[3];
 };
 
-__device__ __forceinline__ uint32_t cvt_e4m3x2(uint32_t v) {  // low 16 bits
-    uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)v));
-    return r;
+// four E4M3 values to two pairs of fp16
+__device__ __forceinline__ void cvt_e4m3x4(uint32_t v, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(v));
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     uint32_t r;
@@ -606,8 +607,7 @@ __global__ void __launch_bounds__(kThreads, cache_attn_ctas(NT))
                             for (int y = 0; y < 2; ++y) {
                                 const uint32_t w = e < 2 ? (e == 0 ? k[n][y].x : k[n][y].y)
                                                          : (e == 2 ? k[n][y].z : k[n][y].w);
-                                a[y] = cvt_e4m3x2(w);
-                                a[y + 2] = cvt_e4m3x2(w >> 16);
+                                cvt_e4m3x4(w, a[y], a[y + 2]);
                             }
 #pragma unroll
                             for (int t = 0; t < NT; ++t) mma16816(c[n][t], a, b[t][0], b[t][1]);
@@ -706,10 +706,8 @@ __global__ void __launch_bounds__(kThreads, cache_attn_ctas(NT))
                     const auto operand = [](const uint32_t (&v)[4][4], int w, int hi, uint32_t (&a)[4]) {
                         const uint32_t x0 = __byte_perm(v[0][w], v[1][w], hi ? 0x7362 : 0x5140);
                         const uint32_t x1 = __byte_perm(v[2][w], v[3][w], hi ? 0x7362 : 0x5140);
-                        a[0] = cvt_e4m3x2(x0);
-                        a[1] = cvt_e4m3x2(x0 >> 16);
-                        a[2] = cvt_e4m3x2(x1);
-                        a[3] = cvt_e4m3x2(x1 >> 16);
+                        cvt_e4m3x4(x0, a[0], a[1]);
+                        cvt_e4m3x4(x1, a[2], a[3]);
                     };
                     if (!slow) {
 #pragma unroll

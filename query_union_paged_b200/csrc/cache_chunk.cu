@@ -101,10 +101,11 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-__device__ __forceinline__ uint32_t cvt_e4m3x2(uint32_t v) {  // low 16 bits
-    uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)v));
-    return r;
+// four E4M3 values to two pairs of fp16
+__device__ __forceinline__ void cvt_e4m3x4(uint32_t v, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(v));
 }
 __device__ __forceinline__ void f16x2_to_f32(uint32_t v, float& lo, float& hi) {
     asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
@@ -609,10 +610,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
 #pragma unroll
                         for (int u = 0; u < kConvRows; ++u) {
-                            const uint4 o0 = make_uint4(cvt_e4m3x2(raw[u].x), cvt_e4m3x2(raw[u].x >> 16),
-                                                        cvt_e4m3x2(raw[u].y), cvt_e4m3x2(raw[u].y >> 16));
-                            const uint4 o1 = make_uint4(cvt_e4m3x2(raw[u].z), cvt_e4m3x2(raw[u].z >> 16),
-                                                        cvt_e4m3x2(raw[u].w), cvt_e4m3x2(raw[u].w >> 16));
+                            uint4 o0, o1;
+                            cvt_e4m3x4(raw[u].x, o0.x, o0.y);
+                            cvt_e4m3x4(raw[u].y, o0.z, o0.w);
+                            cvt_e4m3x4(raw[u].z, o1.x, o1.y);
+                            cvt_e4m3x4(raw[u].w, o1.z, o1.w);
                             // 64 columns in each half; lanes of the two halves store their chunks in
                             // opposite order, so a quarter warp's eight stores meet different banks
                             const bool hi = ch >= 4;
@@ -695,8 +697,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                             __uint_as_float(bb << 16) * up, __uint_as_float(bb & 0xffff0000u) * up};
                         hi[e] = pack_e4m3x4(y[0], y[1], y[2], y[3]);
                         float z[4];
-                        f16x2_to_f32(cvt_e4m3x2(hi[e]), z[0], z[1]);
-                        f16x2_to_f32(cvt_e4m3x2(hi[e] >> 16), z[2], z[3]);
+                        uint32_t h01, h23;
+                        cvt_e4m3x4(hi[e], h01, h23);
+                        f16x2_to_f32(h01, z[0], z[1]);
+                        f16x2_to_f32(h23, z[2], z[3]);
                         lo[e] = pack_e4m3x4(y[0] - z[0], y[1] - z[1], y[2] - z[2], y[3] - z[3]);
                     }
                     __syncwarp();  // both rows have been read
