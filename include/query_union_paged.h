@@ -431,9 +431,10 @@ int qup_cache_append(const qup_cache* cache, const void* k_new, const void* v_ne
  *   max_q      queries of one request, at most
  *   topk, Ksel device int32 [Hq][Nq][Ksel] logical pages of the query's own
  *              request, -1 = padding (duplicates count once), or NULL for all
- *              pages; Hq / Hkv <= 32 with topk
- *   O          device bf16 [Nq][Hq][128], 16-byte aligned; rows of no request
- *              are not written; a row that sees nothing gets 0
+ *              pages (Ksel = 0 with a pointer selects none); Hq / Hkv <= 32 with
+ *              topk
+ *   O          device bf16 [Nq][Hq][128], 16-byte aligned, apart from Q; rows
+ *              of no request are not written; a row that sees nothing gets 0
  *   lse        device fp32 [Nq][Hq] natural-log sum of exponentials (-inf for a
  *              row that sees nothing), or NULL
  *   page_weight device fp32 [total_pages][Hkv] or NULL: the softmax weight that
@@ -473,8 +474,8 @@ int qup_cache_attn(const qup_cache* cache, const void* Q, int64_t q_stride, cons
  *              fp32 [total_pages], the scores in the new order (0 for dropped
  *              pages, acc for unused entries); len_out device int32 [R], the
  *              new kv_len; page_src device int32 [total_pages], the old
- *              request-local place of each entry.  They may be cache's own
- *              page_table and kv_len, and acc.  Entries of no request are left
+ *              request-local place of each entry.  They are apart from each
+ *              other, but may be cache's own page_table and kv_len, and acc.  Entries of no request are left
  *              as they are.
  * Device errors: QUP_ERR_GROUP (contradictory request) and QUP_ERR_CAPACITY
  * (more than max_pages pages): the request's entries are copied unchanged.

@@ -595,7 +595,7 @@ def cache_attn(cache: KVCache, Q, q_ptr, max_q: int, topk=None, softmax_scale: O
     if topk is not None:
         ksel = topk.shape[-1]
         _whole(topk, "topk", torch.int32, (Hq, Nq, ksel), index)
-        topk_p = topk.data_ptr()
+        topk_p = topk.data_ptr() or q_ptr.data_ptr()  # no entries: any address says that it is a TopK call
     if out is None:
         out = torch.empty(shape, dtype=torch.bfloat16, device=Q.device)
     else:

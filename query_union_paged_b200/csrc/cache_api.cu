@@ -145,6 +145,7 @@ int qup_cache_attn(const qup_cache* cache, const void* Q, int64_t q_stride, cons
     if (check_cache_pointers(cache) || !Q || !q_ptr || !O || !ws) return QUP_ERR_ARG;
     if ((reinterpret_cast<uintptr_t>(Q) | reinterpret_cast<uintptr_t>(O) | reinterpret_cast<uintptr_t>(ws)) & 15)
         return QUP_ERR_ARG;
+    if (O == Q) return QUP_ERR_ARG;  // rows of Q are read after others of O are written
     const AttnWs L = attn_ws_layout(cache, Nq, max_q, Hq, page_weight != nullptr);
     if (ws_bytes < L.total) return QUP_ERR_CAPACITY;
 

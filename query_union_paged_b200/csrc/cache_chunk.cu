@@ -26,7 +26,7 @@
 // it and remember its column's first such token; the epilogue gives NaN to the rows that see it.
 //
 // Bound: a step of 256 rows takes about 4,600 cycles.  The two warpgroups' softmax takes 2,500 to 3,200 of
-// them together (their exponentials alone 1,800 to 2,100, of which the MUFU unit 1,540), the tensor
+// them together (their exponentials alone 1,800 to 2,100, of which the MUFU unit 1,790), the tensor
 // cores 2,050; what does not overlap is the way from P to the next S (O update, S, two completions of
 // 200 to 400 cycles each).  1,024 queries x 32 heads behind 16K tokens: 335 us, 0.85 PFLOP/s.
 // Measured and left out: loops unrolled over a step (instruction fetch: +23 %), the warpgroups taking
@@ -58,7 +58,7 @@ constexpr int kMarks = 5;                   // segments whose NaN marks are held
 constexpr int kMaxPages = kStep / 16;
 constexpr int kMmaWarp = 8, kLoadWarp = 9, kConvWarp = 10, kConvWarps = 2;
 constexpr uint32_t kColO = 0, kColS = 256;
-constexpr int kPolyPairs = 2;      // of every eight pairs of exponentials, those on the FMA pipe
+constexpr int kPolyPairs = 1;      // of every eight pairs of exponentials, those on the FMA pipe
 constexpr float kOffset = 8.f;     // log2 offset of P
 constexpr float kLazy = 7.f;       // the maximum moves once a score passes it by this: P <= 2^15
 constexpr float kZeroScaleLog2 = -64.f;

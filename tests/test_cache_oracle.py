@@ -119,7 +119,7 @@ def test_attention_refusals_before_any_device_work():
         assert call(ck) == ARG and size(ck) == ARG, ck
     for kw in (dict(q=None), dict(qs=4088), dict(qs=4100), dict(ptr=None), dict(Nq=-1), dict(max_q=6), dict(Hq=30),
                dict(Hq=0), dict(d=64), dict(K=3), dict(topk=A[5], K=-1), dict(sc=0.0), dict(sc=float("nan")),
-               dict(sc=float("inf")), dict(o=None), dict(wsp=None), dict(o=ctypes.c_void_p(0x20008)),
+               dict(sc=float("inf")), dict(o=None), dict(wsp=None), dict(o=A[0]), dict(o=ctypes.c_void_p(0x20008)),
                dict(topk=A[5], K=9, Hq=8 * 33, qs=8 * 33 * 128), dict(ck=dict(kv_len=0))):
         assert call(**kw) == ARG, kw
     assert call(n=plain - 1) == CAP and call(w=A[6], n=plain) == CAP and call(w=A[6], n=weighted) == NODEV

@@ -420,6 +420,20 @@ def test_topk_pages_match_the_oracle(T, g, K, ns):
     _check_attn(o, lse, w, ref, 1500, (T, g, K))
 
 
+def test_topk_of_no_entries_sees_nothing_and_output_in_place_of_q_is_refused():
+    torch = _t()
+    c = Case(32, [40, 300], T=16)
+    _, qt = _bf16(c.rng.standard_normal((2, 8, 128)))
+    ptr = torch.arange(3, dtype=torch.int32, device="cuda")
+    lse = torch.zeros(2, 8, device="cuda")
+    w = torch.full((len(c.table), 2), 3.0, device="cuda")
+    o = qup.cache_attn(c.cache(), qt, ptr, 1, topk=torch.empty(8, 2, 0, dtype=torch.int32, device="cuda"), lse=lse,
+                       page_weight=w)
+    assert torch.all(o == 0) and torch.all(lse == -math.inf) and torch.all(w == 0) and qup.get_error() == 0
+    with pytest.raises(qup.QupError):
+        qup.cache_attn(c.cache(), qt, ptr, 1, out=qt)
+
+
 def test_topk_of_many_queries_and_pages_behind_the_query():
     c = Case(31, [400, 300], T=16)
     ns = [60, 45]
