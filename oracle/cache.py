@@ -115,7 +115,8 @@ def attn(q, K, V, k_scale, v_scale, page_table, page_ptr, kv_len, q_ptr, softmax
                         continue
                     s = (k[tok] @ q[row, hq]) * softmax_scale
                     m = s.max()
-                    e = np.exp(s - m)
+                    with np.errstate(invalid="ignore"):  # an infinite score
+                        e = np.exp(s - m)
                     lse[row, hq] = m + math.log(e.sum()) if np.isfinite(e.sum()) else math.nan
                     p = e / e.sum()
                     O[row, hq] = p @ v[tok]
