@@ -19,6 +19,7 @@ runs, chunks) and evicted on the device.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 import math
@@ -527,6 +528,13 @@ class KVCache:
         self._ref = ctypes.byref(self._c)
 
 
+def _made_on(stream):
+    """Buffers made inside belong to the call's stream: torch's allocator then hands their memory out again in
+    that stream's order, and not to the current stream while the call is still queued on the other one."""
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def _launch(fn, where: str, index: int, stream, *args):
     """fn(*args, stream) with the cache's device current; stream: a torch stream, or None for that device's
     current one."""
@@ -583,7 +591,8 @@ def cache_attn(cache: KVCache, Q, q_ptr, max_q: int, topk=None, softmax_scale: O
     Q [Nq][Hq][128] bf16 (a query's heads contiguous); q_ptr int32 [R+1]: rows q_ptr[r] .. q_ptr[r+1) are
     request r's last positions, at most max_q of them; topk int32 [Hq][Nq][Ksel] logical pages of the query's
     request (-1 = padding) or None for all pages.  Fills lse fp32 [Nq][Hq] and page_weight fp32
-    [total_pages][Hkv] if given.  Returns O [Nq][Hq][128] bf16.
+    [total_pages][Hkv] if given.  Returns O [Nq][Hq][128] bf16.  An output or workspace that is not given is
+    made on `stream`.
     """
     import torch
     index = cache._index
@@ -597,7 +606,8 @@ def cache_attn(cache: KVCache, Q, q_ptr, max_q: int, topk=None, softmax_scale: O
         _whole(topk, "topk", torch.int32, (Hq, Nq, ksel), index)
         topk_p = topk.data_ptr() or q_ptr.data_ptr()  # no entries: any address says that it is a TopK call
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=Q.device)
+        with _made_on(stream):
+            out = torch.empty(shape, dtype=torch.bfloat16, device=Q.device)
     else:
         _whole(out, "out", torch.bfloat16, shape, index)
     if lse is not None:
@@ -607,7 +617,8 @@ def cache_attn(cache: KVCache, Q, q_ptr, max_q: int, topk=None, softmax_scale: O
         _whole(page_weight, "page_weight", torch.float32, (cache.total_pages, cache.Hkv), index)
         weight_p = page_weight.data_ptr()
     if workspace is None:
-        workspace = cache_attn_workspace(cache, Nq, Hq, max_q, page_weight is not None)
+        with _made_on(stream):
+            workspace = cache_attn_workspace(cache, Nq, Hq, max_q, page_weight is not None)
     size = workspace.numel()
     _whole(workspace, "workspace", torch.uint8, (size,), index)
     _launch((_lib or load()).qup_cache_attn, "qup_cache_attn", index, stream, cache._ref, Q.data_ptr(),
@@ -625,15 +636,17 @@ def cache_evict(cache: KVCache, page_weight, acc, budget: int, sink: int = 1, re
     gathered before.  A request with more than `budget` pages drops the lowest of decay * acc + sum of
     page_weight, but none of its first `sink` and last `recent`.  Returns (page_table, acc, kv_len, page_src),
     the compacted table, accumulator and lengths and each entry's old place in its request; `out` holds these
-    four tensors if given, which may be the cache's own page_table and kv_len, and acc.
+    four tensors if given, which may be the cache's own page_table and kv_len, and acc; else they are made on
+    `stream`.
     """
     import torch
     index, n = cache._index, cache.total_pages
     _whole(page_weight, "page_weight", torch.float32, (n, cache.Hkv), index)
     _whole(acc, "acc", torch.float32, (n,), index)
     if out is None:
-        out = (torch.empty_like(cache.page_table), torch.empty_like(acc), torch.empty_like(cache.kv_len),
-               torch.empty_like(cache.page_table))
+        with _made_on(stream):
+            out = (torch.empty_like(cache.page_table), torch.empty_like(acc), torch.empty_like(cache.kv_len),
+                   torch.empty_like(cache.page_table))
     table, acc_out, lens, src = out
     _whole(table, "out page_table", torch.int32, (n,), index)
     _whole(acc_out, "out acc", torch.float32, (n,), index)

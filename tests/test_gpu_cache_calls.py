@@ -1,0 +1,69 @@
+"""Calls of the 8-bit cache that its documentation allows beside those of test_gpu_cache.py: other streams
+with buffers of the call's own, odd scales, requests that contradict themselves, waits that run out."""
+import math
+
+import numpy as np
+import pytest
+
+import oracle.cache as oc
+import query_union_paged_b200 as qup
+from test_gpu_cache import Case, _bf16, _check_attn, _ptr, _run_attn
+
+pytestmark = pytest.mark.gpu
+
+
+def _t():
+    import torch
+    return torch
+
+
+# ------------------------------------------------------------------ buffers that the call makes
+
+@pytest.mark.parametrize("n", [1, 20])  # the small kernel, and the chunk kernel
+def test_buffers_of_a_call_on_another_stream_belong_to_it(monkeypatch, n):
+    """A workspace or an output that cache_attn or cache_evict makes for a call on another stream is not memory
+    that the current stream has in use or is handed next."""
+    torch = _t()
+    c = Case(91, [400, 300], T=64)
+    cache, ptr = c.cache(), torch.tensor([0, n, 2 * n], dtype=torch.int32, device="cuda")
+    _, q = _bf16(c.rng.standard_normal((2 * n, 8, 128)))
+    want = qup.cache_attn(cache, q, ptr, n)
+    w, acc = torch.rand(len(c.table), 2, device="cuda"), torch.rand(len(c.table), device="cuda")
+    kept = qup.cache_evict(cache, w, acc, 3)
+    torch.cuda.synchronize()
+    made = []
+    real = qup.cache_attn_workspace
+
+    def recorded(*args, **kw):
+        made.append(real(*args, **kw))
+        return made[-1]
+    monkeypatch.setattr(qup, "cache_attn_workspace", recorded)
+    s = torch.cuda.Stream()
+    free = [torch.empty_like(t) for t in (want, *kept)]  # blocks that the current stream may still have in use
+    used = {t.data_ptr() for t in free}
+    del free
+    o = qup.cache_attn(cache, q, ptr, n, stream=s)
+    assert o.data_ptr() not in used
+    size, at = made[0].numel(), made[0].data_ptr()
+    made.clear()
+    assert torch.empty(size, dtype=torch.uint8, device="cuda").data_ptr() != at
+    out = qup.cache_evict(cache, w, acc, 3, stream=s)
+    assert not used & {t.data_ptr() for t in out}
+    torch.cuda.synchronize()
+    assert torch.equal(o, want) and all(torch.equal(a, b) for a, b in zip(out, kept)) and qup.get_error() == 0
+
+
+def test_two_streams_at_once_without_buffers_of_their_own():
+    torch = _t()
+    rng = np.random.default_rng(92)
+    c = Case(92, [int(x) for x in rng.integers(1500, 3000, 12)], T=64)
+    cache, ptr = c.cache(), torch.arange(13, dtype=torch.int32, device="cuda")
+    q = [_bf16(rng.standard_normal((12, 8, 128)))[1] for _ in range(2)]
+    want = [qup.cache_attn(cache, x, ptr, 1) for x in q]
+    streams = [torch.cuda.Stream() for _ in q]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = [qup.cache_attn(cache, x, ptr, 1, stream=s) for s, x in zip(streams, q)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert qup.get_error() == 0
