@@ -758,8 +758,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const auto page = [&](int q2) {
                     float4 v = sm.page[q2];
                     v.x *= rs;
-                    // one of a zero scale stays away from 0, as -inf times it has to be -inf
-                    if (fabsf(v.x) < 1e-30f) v.x = 1e-30f;
+                    // one next to nothing (a scale or a row of zeros) stays away from 0, on the side that mask()
+                    // takes the scale to be: unseen scores are infinities, and times it have to be -inf
+                    if (fabsf(v.x) < 1e-30f) v.x = sm.page[q2].x < 0.f ? -1e-30f : 1e-30f;
                     return v;
                 };
                 float bm = kNegInf;

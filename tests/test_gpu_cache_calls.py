@@ -67,3 +67,23 @@ def test_two_streams_at_once_without_buffers_of_their_own():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert qup.get_error() == 0
+
+
+# ------------------------------------------------------------------ scales
+
+def test_zero_and_tiny_query_rows_over_negative_scales():
+    """Rows of zeros (padding) and of tiny elements, whose score factor is next to nothing, where pages with a
+    negative, a -0 and a subnormal negative K scale hold tokens that they do not see."""
+    c = Case(93, [200, 90, 130], T=32)
+    p0, p1, p2 = (c.table[a:] for a in c.page_ptr[:3])
+    c.ks[p0[5]] *= -1          # request 0's queries are at 160 .. 199
+    c.ks[p0[6]] = -0.0
+    c.ks[p1[1]] = -1e-40       # request 1's at 50 .. 89
+    c.ks[p1[2]] *= -1
+    c.ks[p2[4]] *= -1e-20      # request 2's at 90 .. 129
+    q = 1.5 * c.rng.standard_normal((120, 8, 128))
+    q[[0, 5, 39, 40, 50, 79, 90, 119]] = 0
+    q[7, 3], q[44, 6] = 0, 0
+    q[[3, 60, 100]] *= 2.0 ** -112
+    o, lse, w, ref = _run_attn(c, [40, 40, 40], 4, q=q)
+    _check_attn(o, lse, w, ref, 200, "zero rows")
