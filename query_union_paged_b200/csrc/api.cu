@@ -757,6 +757,8 @@ unsigned long long wait_limit_ns() {
     return (unsigned long long)(ms > 0 ? ms : 2000) * 1000000ull;
 }
 
+int debug_skip_stage() { return g_skip_stage.load(); }
+
 unsigned long long context_id() {
     typedef CUresult (*GetCurrentFn)(CUcontext*);
     typedef CUresult (*GetIdFn)(CUcontext, unsigned long long*);

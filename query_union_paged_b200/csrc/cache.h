@@ -23,6 +23,7 @@ struct DeviceInfo {
 };
 int device_info(DeviceInfo* out);  // QUP_OK or QUP_ERR_CUDA
 unsigned long long wait_limit_ns();  // limit of a pipeline wait (qup_set_debug)
+int debug_skip_stage();              // stage that is not loaded, -1: none (likewise)
 
 // The cache of R requests: qup_cache of the C ABI.
 struct CacheView {

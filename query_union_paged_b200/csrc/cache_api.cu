@@ -225,6 +225,7 @@ int qup_cache_attn(const qup_cache* cache, const void* Q, int64_t q_stride, cons
     p.ws_bits = reinterpret_cast<uint32_t*>(base + L.bits);
     p.err = dev.err;
     p.wait_limit_ns = qup::wait_limit_ns();
+    p.dbg_skip_stage = qup::debug_skip_stage();
     p.scale_log2 = softmax_scale * 1.4426950408889634f;
     p.Nq = Nq;
     p.max_q = max_q;

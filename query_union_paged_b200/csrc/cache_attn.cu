@@ -100,6 +100,13 @@ __device__ __forceinline__ bool has_nan_byte(uint32_t w) {  // an E4M3 NaN (0x7f
     return (x & 0x80808080u) != 0u;
 }
 
+// A bounded wait that the warp's lanes answer as one: a lane whose own limit had run out would leave the
+// others in shuffles, votes and products of the whole warp.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                          const CacheAttnParams& p) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.err, QUP_ERR_TIMEOUT, p.wait_limit_ns));
+}
+
 // Work units of one row tile of a request, and its row tiles.
 __device__ __forceinline__ int units_of(int len) { return (len + kUnit - 1) / kUnit; }
 __device__ __forceinline__ int tiles_of(int n, int g, int RT) { return (n * g + RT - 1) / RT; }
@@ -423,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, cache_attn_ctas(NT))
                     if (phys < 0) msk = 0;
                 }
                 const uint32_t slot = it % NS, par = (it / NS) & 1;
-                if (!mbar_wait(empty0 + 8 * slot, par ^ 1, abort_flag, p.err, QUP_ERR_TIMEOUT, p.wait_limit_ns)) {
+                if (!warp_wait(empty0 + 8 * slot, par ^ 1, abort_flag, p)) {
                     dead = true;
                     break;
                 }
@@ -443,14 +450,15 @@ __global__ void __launch_bounds__(kThreads, cache_attn_ctas(NT))
                     }
                 }
                 __syncwarp();
-                if (lane == 0) {
+                const bool load = it != (uint32_t)p.dbg_skip_stage;
+                if (lane == 0 && load) {
                     if (bytes) mbar_arrive_expect_tx(full0 + 8 * slot, bytes);
                     else mbar_arrive(full0 + 8 * slot);
                 }
                 __syncwarp();
                 for (int x = 0; x < nbox; ++x) {
                     const int ph = __shfl_sync(0xffffffffu, phys, src + x);
-                    if (ph >= 0 && lane == 0) {
+                    if (ph >= 0 && lane == 0 && load) {
                         const uint32_t dst = sbase + L::ring + slot * 2 * kTile + x * box * kHeadDim;
                         tma_load_4d(dst, &tmK, full0 + 8 * slot, 0, (b % upp) * kUnit, sg.h, ph);
                         tma_load_4d(dst + kTile, &tmV, full0 + 8 * slot, 0, (b % upp) * kUnit, sg.h, ph);
@@ -559,8 +567,7 @@ __global__ void __launch_bounds__(kThreads, cache_attn_ctas(NT))
 #pragma unroll
             for (int n = 0; n < NG; ++n) {
                 const uint32_t slot = (it + n) % NS, par = ((it + n) / NS) & 1;
-                if (!dead && !mbar_wait(full0 + 8 * slot, par, abort_flag, p.err, QUP_ERR_TIMEOUT, p.wait_limit_ns))
-                    dead = true;
+                if (!dead && !warp_wait(full0 + 8 * slot, par, abort_flag, p)) dead = true;
                 pm[n] = meta[slot * kMaxBoxes + 16 * warp / box];
                 pos[n] = pm[n].pos + (16 * warp) % box;
                 live[n] = pm[n].mask != 0u && pos[n] < vis_any;

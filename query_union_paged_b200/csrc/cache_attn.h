@@ -47,6 +47,7 @@ struct CacheAttnParams {
     ChunkSpan* spans;
     unsigned* err;
     unsigned long long wait_limit_ns;
+    int dbg_skip_stage;  // a stage of each CTA that is not loaded, so that its waits run out; -1: none
     float scale_log2;
     int Nq, max_q, Hq, g, Ksel;
     int per_units;   // all pages: least units of a CTA

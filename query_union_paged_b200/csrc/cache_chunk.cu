@@ -451,12 +451,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (lane == 0) mbar_arrive(B.mfull(it % kNM));
                         }
                         const uint32_t full = kv ? B.vfull(slot) : B.kfull(slot);
-                        if (lane == 0) {
+                        const bool load = it != (uint32_t)p.dbg_skip_stage;
+                        if (lane == 0 && load) {
                             if (bytes) mbar_arrive_expect_tx(full, bytes);
                             else mbar_arrive(full);
                         }
                         __syncwarp();
-                        if (lane >= src && lane < src + PPS && phys >= 0)
+                        if (lane >= src && lane < src + PPS && phys >= 0 && load)
                             tma_load_4d(sbase + (kv ? Layout::v : Layout::k) + slot * kTile +
                                             (uint32_t)(lane - src) * T * kHeadDim,
                                         kv ? &tmV : &tmK, full, 0, 0, h, phys);

@@ -87,3 +87,32 @@ def test_zero_and_tiny_query_rows_over_negative_scales():
     q[[3, 60, 100]] *= 2.0 ** -112
     o, lse, w, ref = _run_attn(c, [40, 40, 40], 4, q=q)
     _check_attn(o, lse, w, ref, 200, "zero rows")
+
+
+# ------------------------------------------------------------------ waits that run out
+
+@pytest.mark.parametrize("ns,topk", [([1, 1, 1], None), ([4, 4, 2], None), ([40, 40, 40], None), ([70, 1, 3], None),
+                                     ([1, 1, 1], 6), ([2, 1, 1], 40)])
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(ns, topk):
+    """One stage of every CTA is not loaded: the waits end at their limit, QUP_ERR_TIMEOUT is raised, the
+    kernels leave and the next call gives the bits of an undisturbed one."""
+    torch = _t()
+    c = Case(103, [20000, 9000, 900], T=64)
+    cache, ptr = c.cache(), torch.from_numpy(_ptr(ns)).cuda()
+    _, q = _bf16(c.rng.standard_normal((sum(ns), 8, 128)))
+    tk = None
+    if topk:
+        tk = torch.arange(topk, dtype=torch.int32, device="cuda").remainder(11).expand(8, sum(ns), topk).contiguous()
+    w = [torch.empty(len(c.table), 2, device="cuda") for _ in range(2)]
+    want = qup.cache_attn(cache, q, ptr, max(ns), topk=tk, page_weight=w[0])
+    assert qup.get_error() == 0
+    for stage in (0, 1) if topk is None else (0,):  # a CTA of these TopK calls has one stage
+        try:
+            qup.set_debug(wait_limit_ms=50, skip_stage=stage)
+            qup.cache_attn(cache, q, ptr, max(ns), topk=tk, page_weight=w[1])
+            code = qup.get_error()
+        finally:
+            qup.set_debug(0, -1)
+        assert code == qup.ERR["TIMEOUT"], (stage, code)
+        got = qup.cache_attn(cache, q, ptr, max(ns), topk=tk, page_weight=w[1])
+        assert qup.get_error() == 0 and torch.equal(got, want) and torch.equal(w[0], w[1]), stage
