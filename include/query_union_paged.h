@@ -446,11 +446,12 @@ int qup_cache_append(const qup_cache* cache, const void* k_new, const void* v_ne
  *              preparation and mean nothing after the call.
  * Results do not depend on the run: partial results are merged in a fixed
  * order, without atomics.  Device errors: QUP_ERR_GROUP for a contradictory
- * request or one with more than max_q queries (its rows get O = 0, lse = -inf),
- * QUP_ERR_CAPACITY for a request with more than max_pages pages (likewise),
- * QUP_ERR_PAGE_ID for a TopK entry outside the request's
- * pages (ignored), QUP_ERR_PHYS_PAGE and QUP_ERR_SCALE for a bad page_table
- * entry or scale (the page is not seen), QUP_ERR_TIMEOUT as elsewhere.
+ * request or one with more than max_q queries (all of its rows in [0, Nq) get
+ * O = 0, lse = -inf, its pages the weight 0), QUP_ERR_CAPACITY for a request
+ * with more than max_pages pages (likewise), QUP_ERR_PAGE_ID for a TopK entry
+ * outside the request's pages (ignored), QUP_ERR_PHYS_PAGE and QUP_ERR_SCALE
+ * for a bad page_table entry or scale (the page is not seen), QUP_ERR_TIMEOUT
+ * as elsewhere.
  */
 int qup_cache_attn_workspace(const qup_cache* cache, int Nq, int max_q, int Hq, int page_weight, size_t* ws_bytes);
 int qup_cache_attn(const qup_cache* cache, const void* Q, int64_t q_stride, const int32_t* q_ptr, int Nq, int max_q,

@@ -121,10 +121,6 @@ __device__ __forceinline__ Span my_span(int R) {
     const int a = min(R, (int)threadIdx.x * per);
     return Span{a, min(R, a + per)};
 }
-__device__ __forceinline__ unsigned request_fault(const CacheAttnParams& p, const Request& q) {
-    if (!q.ok || q.n > p.max_q) return QUP_ERR_GROUP;
-    return q.np > p.max_pages ? QUP_ERR_CAPACITY : 0u;
-}
 __device__ __forceinline__ int request_units(const CacheAttnParams& p, int r, int RT, unsigned* bad) {
     const Request q = load_request(p.q_ptr, p.Nq, p.c.kv_len, p.c.page_ptr, p.c.total_pages, p.c.T, r);
     if ((long long)q.n * p.g >= p.big_rows) return 0;  // the chunk kernel's
@@ -302,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, cache_attn_ctas(NT))
                 }
             }
         }
-        __syncthreads();
+        if (__syncthreads_or(bad != 0u)) clear_faulty(p, false);
         if (s_start[2] == 0) return;
     } else {
         // the item's query and request
@@ -903,7 +899,8 @@ __device__ __forceinline__ void merge_row(const CacheAttnParams& p, int q0, int 
 }
 
 // One CTA per item: the partial results of its rows, in the order of the CTAs that left them.  Rows
-// of an item that one CTA finished are left alone; rows that see nothing get O = 0, lse = -inf.
+// of an item that one CTA finished are left alone, as are those of faulty requests; rows that see nothing get
+// O = 0, lse = -inf.
 template <int RT, bool SPARSE>
 __global__ void __launch_bounds__(kHeadDim) cache_merge_kernel(const __grid_constant__ CacheAttnParams p, int grid_x) {
     __shared__ long long red[2][kHeadDim / 32];
@@ -925,19 +922,17 @@ __global__ void __launch_bounds__(kHeadDim) cache_merge_kernel(const __grid_cons
     } else {
         const int per_r = p.c.Hkv * p.max_tiles, r = blockIdx.x / per_r, x = blockIdx.x - r * per_r;
         const Request q = load_request(p.q_ptr, p.Nq, p.c.kv_len, p.c.page_ptr, p.c.total_pages, p.c.T, r);
-        const bool rows_ok =
-            q.q0 >= 0 && q.n >= 0 && (long long)q.q0 + q.n <= p.Nq && (long long)q.n * g < p.big_rows;
-        const bool ok = request_fault(p, q) == 0u;
-        const int nt = rows_ok ? tiles_of(min(q.n, p.max_q), g, RT) : 0;
+        const bool mine = request_fault(p, q) == 0u && (long long)q.n * g < p.big_rows;
+        const int nt = mine ? tiles_of(q.n, g, RT) : 0;
         h = x / p.max_tiles;
         const int tile = x - h * p.max_tiles;
         if (tile >= nt) return;
         q0 = q.q0;
         row0 = tile * RT;
-        rows = min(RT, min(q.n, p.max_q) * g - row0);
-        const int nb = ok ? units_of(q.len) : 0;
+        rows = min(RT, q.n * g - row0);
+        const int nb = units_of(q.len);
         const int vis = q.len - q.n + (row0 + rows - 1) / g + 1;
-        const int nvis = !ok || vis <= 0 ? 0 : units_of(vis);
+        const int nvis = vis <= 0 ? 0 : units_of(vis);
         c0 = 0;
         nc = 0;
         if (nvis > 0) {

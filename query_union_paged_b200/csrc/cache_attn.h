@@ -8,6 +8,8 @@
 #include <cuda_runtime.h>
 
 #include "cache.h"
+#include "internal.h"
+#include "query_union_paged.h"
 
 namespace qup {
 
@@ -57,6 +59,26 @@ struct CacheAttnParams {
     int big_rows;    // all pages: requests of this many rows or more are the chunk kernel's
     int list_cap;    // TopK pages: distinct pages of one CTA, at most
 };
+
+// What keeps a request from being read (0: nothing), as device error bits.
+__device__ __forceinline__ unsigned request_fault(const CacheAttnParams& p, const Request& q) {
+    if (!q.ok || q.n > p.max_q) return QUP_ERR_GROUP;
+    return q.np > p.max_pages ? QUP_ERR_CAPACITY : 0u;
+}
+// Rows of faulty requests (`big`: those that would be the chunk kernel's) get O = 0 and lse = -inf: the CTAs
+// take the requests in turn.
+__device__ __forceinline__ void clear_faulty(const CacheAttnParams& p, bool big) {
+    for (int r = blockIdx.x; r < p.c.R; r += gridDim.x) {
+        const Request q = load_request(p.q_ptr, p.Nq, p.c.kv_len, p.c.page_ptr, p.c.total_pages, p.c.T, r);
+        if (request_fault(p, q) == 0u || ((long long)q.n * p.g >= p.big_rows) != big) continue;
+        const long long a = max(q.q0, 0), b = min((long long)q.q0 + q.n, (long long)p.Nq);
+        uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.O) + (size_t)a * p.Hq * kHeadDim);
+        for (long long x = threadIdx.x; x < (b - a) * p.Hq * (kHeadDim / 8); x += blockDim.x)
+            o[x] = make_uint4(0u, 0u, 0u, 0u);
+        for (long long x = threadIdx.x; p.lse && x < (b - a) * p.Hq; x += blockDim.x)
+            p.lse[a * p.Hq + x] = -INFINITY;
+    }
+}
 
 // nt: row tiles of 8 rows (1, 2 or 4)
 size_t cache_attn_smem(int nt, bool sparse, int max_pages, int list_cap);

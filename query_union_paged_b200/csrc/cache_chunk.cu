@@ -139,32 +139,26 @@ __device__ long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
     return s;
 }
 
-// One request's items.  Row tile t's steps: floor((g (base + 127) + last row) / (128 g)) with base =
-// tokens its first query sees, which is ceil(tokens its last row sees / 128).
+// One request's items (none of a faulty one).  Row tile t's steps: floor((g (base + 127) + last row) /
+// (128 g)) with base = tokens its first query sees, which is ceil(tokens its last row sees / 128).
 struct Items {
     Request q;
     int nt, rows, base;
-    bool ok;
     __device__ __forceinline__ void load(const CacheAttnParams& p, int r, unsigned* fault) {
         q = load_request(p.q_ptr, p.Nq, p.c.kv_len, p.c.page_ptr, p.c.total_pages, p.c.T, r);
-        unsigned f = !q.ok || q.n > p.max_q ? QUP_ERR_GROUP : 0u;
-        if (!f && q.np > p.max_pages) f = QUP_ERR_CAPACITY;
+        const unsigned f = request_fault(p, q);
         *fault |= f;
-        ok = f == 0u;
-        const bool rows_ok = q.q0 >= 0 && q.n > 0 && (long long)q.q0 + q.n <= p.Nq;
-        rows = rows_ok ? min(q.n, p.max_q) * p.g : 0;
+        rows = f ? 0 : q.n * p.g;
         if (rows < p.big_rows) rows = 0;  // the other kernel's
         nt = (rows + kItemRows - 1) / kItemRows;
-        base = ok ? max(q.len - q.n, 0) + 1 : 0;
+        base = max(q.len - q.n, 0) + 1;
     }
     __device__ __forceinline__ int steps(const CacheAttnParams& p, int t) const {
-        if (!ok) return 1;
         const int last = min((t + 1) * kItemRows, rows) - 1;
         return (int)((uint32_t)(p.g * (base + kStep - 1) + last) / (uint32_t)(kStep * p.g));
     }
     // steps of the first t < nt row tiles
     __device__ __forceinline__ long long before(const CacheAttnParams& p, int t) const {
-        if (!ok) return t;
         return floor_sum(t, kStep * p.g, kItemRows, p.g * (base + kStep - 1) + kItemRows - 1);
     }
     __device__ __forceinline__ long long total(const CacheAttnParams& p) const {
@@ -377,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 at += u;
             }
         }
-        __syncthreads();
+        if (__syncthreads_or(fault != 0u)) clear_faulty(p, true);
     }
 
     WarpWalk& ww = *reinterpret_cast<WarpWalk*>(smem + Layout::walks + warp * 128);
@@ -399,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 info.ends = sg.b1 == sg.steps;
                 if (info.segs == 0) info.first_ends = info.ends;
                 ++info.segs;
-                const int b1 = sg.b1, h = sg.h, last = wk.it.ok ? (wk.it.q.len + T - 1) / T : 0, p0 = wk.it.q.p0;
+                const int b1 = sg.b1, h = sg.h, last = (wk.it.q.len + T - 1) / T, p0 = wk.it.q.p0;
                 int have0 = 0, have1 = 0, phys = -1;  // page table entries that the lanes hold
                 float ks = 0.f, vl = 0.f, vi = 0.f;
                 for (int b = sg.b0; b < b1 && ok; ++b, ++it) {
@@ -656,8 +650,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool on = r < rows;
             const int x = row0 + (on ? r : rows - 1), qi = x / g, j = x - qi * g;
             // tokens this row sees, and the warpgroup's first row
-            const int vis = wk.it.ok ? wk.it.q.len - wk.it.q.n + qi + 1 : 0;
-            const int vis_all = wk.it.ok ? wk.it.q.len - wk.it.q.n + row0 / g + 1 : 0;
+            const int vis = wk.it.q.len - wk.it.q.n + qi + 1;
+            const int vis_all = wk.it.q.len - wk.it.q.n + row0 / g + 1;
             // ---- Q: high and low E4M3 parts of the warp's rows, each row's score factor.  16 lanes share a
             // row: 8 elements each.  The bf16 rows come into the places that their two parts will take.
             float rs = 0.f;
@@ -718,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int b0 = sg.b0, b1 = sg.b1;
             float2* mass_row = nullptr;  // page weights: this row's sums, rowsw * T / 16 apart per page
             int mass_pages = 0;
-            if (WEIGHTS && on && wk.it.ok) {
+            if (WEIGHTS && on) {
                 const Request& q = wk.it.q;
                 mass_row = p.ws_mass + ((size_t)q.p0 * p.c.Hkv + (size_t)sg.h * q.np) * (T / 16) * ((size_t)p.max_q * g) + x;
                 mass_pages = (q.len + T - 1) / T;
@@ -967,7 +961,7 @@ __global__ void __launch_bounds__(kHeadDim) cache_chunk_join_kernel(const __grid
     const ChunkSpan a = p.spans[blockIdx.x];
     if (a.segs == 0 || a.ends || a.b0 != 0) return;
     const Request q = load_request(p.q_ptr, p.Nq, p.c.kv_len, p.c.page_ptr, p.c.total_pages, p.c.T, a.r);
-    const int rows = min(kItemRows, min(q.n, p.max_q) * p.g - a.tile * kItemRows);
+    const int rows = min(kItemRows, q.n * p.g - a.tile * kItemRows);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int last = blockIdx.x + 1;
     while (last < runs - 1 && !p.spans[last].first_ends) ++last;

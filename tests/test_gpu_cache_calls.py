@@ -89,6 +89,63 @@ def test_zero_and_tiny_query_rows_over_negative_scales():
     _check_attn(o, lse, w, ref, 200, "zero rows")
 
 
+# ------------------------------------------------------------------ requests that contradict themselves
+
+def _faulty(c, ns, max_q, bad, g=4, lens=None, cut=0, topk=None, max_pages=None, code="GROUP"):
+    """Rows of the requests `bad` get O = 0 and lse = -inf, rows of no request are left alone, the others'
+    results are the oracle's.  lens: kv_len on the device; cut: rows that Q has fewer than q_ptr says."""
+    torch = _t()
+    ptr = _ptr(ns)
+    N = int(ptr[-1]) - cut
+    qv, qt = _bf16(c.rng.standard_normal((int(ptr[-1]) + 2, 2 * g, 128)))
+    rows = N + (0 if cut else 2)  # two rows of no request
+    qt = qt[:rows].contiguous()
+    kw = {} if max_pages is None else dict(max_pages=max_pages)
+    cache = c.cache(**kw)
+    if lens is not None:
+        cache.kv_len.copy_(torch.tensor(lens, dtype=torch.int32))
+    o = torch.full((rows, 2 * g, 128), 5.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((rows, 2 * g), 5.0, device="cuda")
+    w = torch.full((len(c.table), 2), 5.0, device="cuda")
+    tk = None
+    if topk:
+        tk = torch.arange(topk, dtype=torch.int32, device="cuda").expand(2 * g, rows, topk).contiguous()
+    qup.cache_attn(cache, qt, torch.from_numpy(ptr).cuda(), max_q, topk=tk, out=o, lse=lse, page_weight=w)
+    assert qup.get_error() == qup.ERR[code]
+    sel = None if tk is None else tk.cpu().numpy()
+    full = oc.attn(np.concatenate([qv, qv])[:int(ptr[-1])], c.K, c.V, c.ks, c.vs, c.table, c.page_ptr, c.lens, ptr,
+                   1 / math.sqrt(128), None if sel is None else np.resize(sel[:, :1], (2 * g, int(ptr[-1]), topk)))
+    og, lg, wg = o.double().cpu().numpy(), lse.double().cpu().numpy(), w.cpu().numpy()
+    for r in range(len(ns)):
+        a, b = int(ptr[r]), min(int(ptr[r + 1]), rows)
+        pages = slice(int(c.page_ptr[r]), int(c.page_ptr[r + 1]))
+        if r in bad:
+            assert np.all(og[a:b] == 0) and np.all(np.isneginf(lg[a:b])), r
+            assert np.all(wg[pages] == 0), r
+        else:
+            ref = {k: v[a:b] for k, v in full.items() if k != "weight"}
+            _check_attn(og[a:b], lg[a:b], None, ref, int(c.lens[r]), r)
+    if not cut:
+        assert np.all(og[N:] == 5) and np.all(lg[N:] == 5)
+
+
+@pytest.mark.parametrize("n,topk", [(1, None), (4, None), (40, None), (2, 3)])
+def test_every_row_of_a_faulty_request_is_zero(n, topk):
+    lens = [300, 200, 250, 190]
+    case = lambda: Case(97, lens, T=64)
+    _faulty(case(), [n, 3 * n + 1, n, n], n, [1], topk=topk)                   # more queries than max_q
+    _faulty(case(), [n, n, n, n], n, [2], lens=[300, 200, 10 ** 6, 190], topk=topk)  # more tokens than pages
+    _faulty(case(), [n, n, n, n + 1], n + 1, [3], cut=1, topk=topk)            # rows past the batch
+    _faulty(Case(98, [300, 200, 700, 190], T=64), [n] * 4, n, [2], max_pages=6, topk=topk, code="CAPACITY")
+
+
+def test_faulty_requests_among_small_and_large_ones():
+    c = Case(99, [300, 400, 250, 190, 60, 600], T=64)
+    _faulty(c, [2, 70, 30, 3, 1, 40], 40, [1, 4], lens=[300, 400, 250, 190, 10 ** 6, 600])
+    c = Case(99, [300, 400, 250, 190, 60, 600], T=64)
+    _faulty(c, [40, 3, 41, 4, 40, 2], 40, [2, 3], lens=[300, 400, 250, 10 ** 6, 60, 600])
+
+
 # ------------------------------------------------------------------ waits that run out
 
 @pytest.mark.parametrize("ns,topk", [([1, 1, 1], None), ([4, 4, 2], None), ([40, 40, 40], None), ([70, 1, 3], None),
