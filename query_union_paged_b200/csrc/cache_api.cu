@@ -160,7 +160,7 @@ int qup_cache_attn(const qup_cache* cache, const void* Q, int64_t q_stride, cons
     qup::CacheAttnParams p;
     std::memset(&p, 0, sizeof(p));
     p.big_rows = !chunk ? 0x7fffffff : (small ? qup::kCacheSmallRows + 1 : 1);
-    p.max_tiles = (int)((small_rows + rt - 1) / rt);
+    p.max_tiles = (int)std::max<int64_t>((small_rows + rt - 1) / rt, 1);  // max_q = 0: a request's rows are a fault
     const int64_t max_units = ((int64_t)c.max_pages * c.T + qup::kCacheUnit - 1) / qup::kCacheUnit;
     // the chunk kernel counts steps and a request's rows in 32 bits
     if (chunk && (((int64_t)c.max_pages * c.T + 256 + max_q) * g + 256 >= ((int64_t)1 << 31) ||

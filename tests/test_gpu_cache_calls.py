@@ -146,6 +146,23 @@ def test_faulty_requests_among_small_and_large_ones():
     _faulty(c, [40, 3, 41, 4, 40, 2], 40, [2, 3], lens=[300, 400, 250, 10 ** 6, 60, 600])
 
 
+def test_no_queries_of_any_request():
+    """max_q = 0: a batch of nothing but padding rows; a request that has rows all the same is faulty."""
+    torch = _t()
+    c = Case(100, [100, 40], T=16)
+    _, qt = _bf16(c.rng.standard_normal((3, 8, 128)))
+    for topk in (None, torch.zeros(8, 3, 2, dtype=torch.int32, device="cuda")):
+        o = torch.full((3, 8, 128), 5.0, dtype=torch.bfloat16, device="cuda")
+        lse, w = torch.full((3, 8), 5.0, device="cuda"), torch.full((len(c.table), 2), 5.0, device="cuda")
+        qup.cache_attn(c.cache(), qt, torch.zeros(3, dtype=torch.int32, device="cuda"), 0, topk=topk, out=o, lse=lse,
+                       page_weight=w)
+        assert qup.get_error() == 0 and torch.all(o == 5) and torch.all(lse == 5) and torch.all(w == 0)
+        qup.cache_attn(c.cache(), qt, torch.tensor([0, 0, 2], dtype=torch.int32, device="cuda"), 0, topk=topk, out=o,
+                       lse=lse, page_weight=w)
+        assert qup.get_error() == qup.ERR["GROUP"] and torch.all(o[:2] == 0) and torch.all(lse[:2] == -math.inf)
+        assert torch.all(o[2] == 5) and torch.all(w == 0)
+
+
 # ------------------------------------------------------------------ waits that run out
 
 @pytest.mark.parametrize("ns,topk", [([1, 1, 1], None), ([4, 4, 2], None), ([40, 40, 40], None), ([70, 1, 3], None),
