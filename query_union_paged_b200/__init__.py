@@ -574,13 +574,15 @@ def cache_append(cache: KVCache, k_new, v_new, tok_ptr, stream=None):
             v_new.data_ptr(), BF16 if dtype is torch.bfloat16 else F32, ks, vs, tok_ptr.data_ptr(), N, 128)
 
 
-def cache_attn_workspace(cache: KVCache, Nq: int, Hq: int, max_q: int, page_weight: bool = False):
+def cache_attn_workspace(cache: KVCache, Nq: int, Hq: int, max_q: int, page_weight: bool = False, topk: bool = True):
     """A workspace for cache_attn calls of these sizes on this cache (qup_cache_attn_workspace).  Calls that
-    may run at the same time, captured graphs among them, need one each."""
+    may run at the same time, captured graphs among them, need one each.  With page_weight, topk=False makes one
+    for calls without topk only: up to T / 16 times smaller where requests are long.
+    """
     import torch
     n = ctypes.c_size_t(0)
-    _check(load().qup_cache_attn_workspace(cache._ref, Nq, max_q, Hq, 1 if page_weight else 0, ctypes.byref(n)),
-           "qup_cache_attn_workspace")
+    _check(load().qup_cache_attn_workspace(cache._ref, Nq, max_q, Hq, (1 if topk else 2) if page_weight else 0,
+                                           ctypes.byref(n)), "qup_cache_attn_workspace")
     return torch.empty(n.value, dtype=torch.uint8, device=cache.device)
 
 
@@ -618,7 +620,7 @@ def cache_attn(cache: KVCache, Q, q_ptr, max_q: int, topk=None, softmax_scale: O
         weight_p = page_weight.data_ptr()
     if workspace is None:
         with _made_on(stream):
-            workspace = cache_attn_workspace(cache, Nq, Hq, max_q, page_weight is not None)
+            workspace = cache_attn_workspace(cache, Nq, Hq, max_q, page_weight is not None, topk is not None)
     size = workspace.numel()
     _whole(workspace, "workspace", torch.uint8, (size,), index)
     _launch((_lib or load()).qup_cache_attn, "qup_cache_attn", index, stream, cache._ref, Q.data_ptr(),

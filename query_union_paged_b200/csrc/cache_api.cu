@@ -49,14 +49,43 @@ qup::CacheView view_of(const qup_cache* c) {
 
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-struct AttnWs {
-    size_t part_o, part_ml, chunk_o, chunk_ml, spans, mass, lse, bits, total;
+// All pages: requests of up to kCacheSmallRows rows (queries x heads of a KV head) go to the kernel
+// of the small ones, the others to the chunk kernel.  Where every request has max_q queries or
+// the batch is padded, one kernel takes them all.
+struct AttnPlan {
+    bool chunk, small;
+    int64_t small_rows;  // rows of a request of the small kernel, at most
 };
+AttnPlan attn_plan(const qup_cache* c, int Nq, int max_q, int Hq, bool sparse) {
+    const int g = Hq / c->Hkv;
+    const int64_t big = (int64_t)max_q * g;
+    AttnPlan a;
+    a.chunk = !sparse && big > qup::kCacheSmallRows;
+    a.small = !a.chunk || (int64_t)c->R * max_q != Nq;
+    a.small_rows = a.chunk ? qup::kCacheSmallRows : big;
+    return a;
+}
+
+struct AttnWs {
+    size_t part_o, part_ml, chunk_o, chunk_ml, spans, mass, mass_chunk, lse, bits, total;
+    int mass_per, mass_chunk_per;
+};
+
+// Bytes of the page weights' sums, `slots` for a page: by pages with room for `rows` rows of one request
+// (*per), or by rows with room for max_pages pages (*per = 0), see mass_of().  Sizes past 2^62 are cut there.
+size_t mass_bytes(const qup_cache* c, int Nq, int Hq, int64_t rows, int slots, int* per) {
+    typedef unsigned __int128 u128;
+    const u128 by_pages = (u128)c->total_pages * c->Hkv * (u128)rows, by_rows = (u128)Nq * Hq * (u128)c->max_pages;
+    *per = by_pages <= by_rows ? (int)std::max<int64_t>(rows, 1) : 0;
+    return (size_t)std::min<u128>(std::min(by_pages, by_rows) * slots * sizeof(float2), (u128)1 << 62);
+}
 
 // The partial results of an all-pages call: two of each CTA.  Those of a TopK call: one of each CTA
 // of a (query, KV head), which is cut only while all of them fit the SMs at once.
-AttnWs attn_ws_layout(const qup_cache* c, int Nq, int max_q, int Hq, bool weights) {
+AttnWs attn_ws_layout(const qup_cache* c, int Nq, int max_q, int Hq, bool weights, bool sparse) {
     AttnWs w;
+    std::memset(&w, 0, sizeof(w));
+    const AttnPlan plan = attn_plan(c, Nq, max_q, Hq, sparse);
     const size_t parts = qup::kCachePartRows;
     size_t off = 0;
     w.part_o = off;
@@ -64,20 +93,22 @@ AttnWs attn_ws_layout(const qup_cache* c, int Nq, int max_q, int Hq, bool weight
     w.part_ml = off;
     off = align256(off + parts * sizeof(float2));
     const size_t crows = 2 * (size_t)qup::kChunkMaxRuns * qup::kChunkRows;
-    const bool chunks = (int64_t)max_q * (Hq / c->Hkv) > qup::kCacheSmallRows;
     w.chunk_o = off;
-    if (chunks) off = align256(off + crows * qup::kHeadDim * sizeof(float));
+    if (plan.chunk) off = align256(off + crows * qup::kHeadDim * sizeof(float));
     w.chunk_ml = off;
-    if (chunks) off = align256(off + crows * sizeof(float2));
+    if (plan.chunk) off = align256(off + crows * sizeof(float2));
     w.spans = off;
-    if (chunks) off = align256(off + qup::kChunkMaxRuns * sizeof(qup::ChunkSpan));
-    w.mass = w.lse = w.bits = off;
+    if (plan.chunk) off = align256(off + qup::kChunkMaxRuns * sizeof(qup::ChunkSpan));
     if (weights) {
-        off = align256(off + sizeof(float2) * (size_t)c->total_pages * (c->T / 16) * Hq * max_q);
+        w.mass = off;
+        if (plan.small) off = align256(off + mass_bytes(c, Nq, Hq, plan.small_rows, c->T / 16, &w.mass_per));
+        w.mass_chunk = off;
+        if (plan.chunk)
+            off = align256(off + mass_bytes(c, Nq, Hq, (int64_t)max_q * (Hq / c->Hkv), 1, &w.mass_chunk_per));
         w.lse = off;
         off = align256(off + sizeof(float) * (size_t)Nq * Hq);
         w.bits = off;
-        off = align256(off + sizeof(uint32_t) * ((size_t)c->total_pages / 32 + c->R) * max_q * c->Hkv);
+        if (sparse) off = align256(off + sizeof(uint32_t) * ((size_t)c->total_pages / 32 + c->R) * max_q * c->Hkv);
     }
     w.total = off;
     return w;
@@ -118,7 +149,12 @@ int qup_cache_append(const qup_cache* cache, const void* k_new, const void* v_ne
 int qup_cache_attn_workspace(const qup_cache* cache, int Nq, int max_q, int Hq, int page_weight, size_t* ws_bytes) {
     const int rc = check_attn_sizes(cache, Nq, max_q, Hq);
     if (rc) return rc;
-    if (ws_bytes) *ws_bytes = attn_ws_layout(cache, Nq, max_q, Hq, page_weight != 0).total;
+    if (page_weight < 0 || page_weight > 2) return QUP_ERR_ARG;
+    if (ws_bytes) {
+        *ws_bytes = attn_ws_layout(cache, Nq, max_q, Hq, page_weight != 0, false).total;
+        if (page_weight != 2)  // TopK calls too
+            *ws_bytes = std::max(*ws_bytes, attn_ws_layout(cache, Nq, max_q, Hq, page_weight != 0, true).total);
+    }
     return QUP_OK;
 }
 
@@ -146,16 +182,12 @@ int qup_cache_attn(const qup_cache* cache, const void* Q, int64_t q_stride, cons
     if ((reinterpret_cast<uintptr_t>(Q) | reinterpret_cast<uintptr_t>(O) | reinterpret_cast<uintptr_t>(ws)) & 15)
         return QUP_ERR_ARG;
     if (O == Q) return QUP_ERR_ARG;  // rows of Q are read after others of O are written
-    const AttnWs L = attn_ws_layout(cache, Nq, max_q, Hq, page_weight != nullptr);
+    const AttnWs L = attn_ws_layout(cache, Nq, max_q, Hq, page_weight != nullptr, sparse);
     if (ws_bytes < L.total) return QUP_ERR_CAPACITY;
 
-    // All pages: requests of up to kCacheSmallRows rows (queries x heads of a KV head) go to the kernel
-    // of the small ones, the others to the chunk kernel.  Where every request has max_q queries or
-    // the batch is padded, one kernel takes them all.
-    const int64_t big = (int64_t)max_q * g;
-    const bool chunk = !sparse && big > qup::kCacheSmallRows;
-    const bool small = !chunk || (int64_t)c.R * max_q != Nq;
-    const int64_t small_rows = sparse ? g : std::min<int64_t>(big, qup::kCacheSmallRows);
+    const AttnPlan plan = attn_plan(cache, Nq, max_q, Hq, sparse);
+    const bool chunk = plan.chunk, small = plan.small;
+    const int64_t small_rows = sparse ? g : plan.small_rows;  // TopK: a query's rows are a tile
     const int nt = small_rows <= 8 ? 1 : (small_rows <= 16 ? 2 : 4), rt = 8 * nt;
     qup::CacheAttnParams p;
     std::memset(&p, 0, sizeof(p));
@@ -220,7 +252,10 @@ int qup_cache_attn(const qup_cache* cache, const void* Q, int64_t q_stride, cons
     p.chunk_o = reinterpret_cast<float*>(base + L.chunk_o);
     p.chunk_ml = reinterpret_cast<float2*>(base + L.chunk_ml);
     p.spans = reinterpret_cast<qup::ChunkSpan*>(base + L.spans);
-    p.ws_mass = reinterpret_cast<float2*>(base + L.mass);
+    p.mass = reinterpret_cast<float2*>(base + L.mass);
+    p.mass_chunk = reinterpret_cast<float2*>(base + L.mass_chunk);
+    p.mass_per = L.mass_per;
+    p.mass_chunk_per = L.mass_chunk_per;
     p.ws_lse = reinterpret_cast<float*>(base + L.lse);
     p.ws_bits = reinterpret_cast<uint32_t*>(base + L.bits);
     p.err = dev.err;

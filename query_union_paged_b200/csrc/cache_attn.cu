@@ -548,10 +548,17 @@ __global__ void __launch_bounds__(kThreads, cache_attn_ctas(NT))
         const uint32_t all_rows = SPARSE ? (rows == 32 ? 0xffffffffu : (1u << rows) - 1u) : 0xffffffffu;
 
         // page weights: this tile's rows, mass_rows apart for every 16 tokens
-        const size_t mass_rows = (size_t)p.max_q * g;
-        float2* const mass = !WEIGHTS ? nullptr
-                                      : p.ws_mass + ((size_t)sg.p0 * p.c.Hkv + (size_t)sg.h * sg.np) * (T / 16) * mass_rows +
-                                            (SPARSE ? (sg.q0 - p.q_ptr[sg.r]) * g : row0);
+        size_t mass_rows = 0;
+        float2* mass = nullptr;
+        if constexpr (WEIGHTS) {
+            Request q{};
+            q.q0 = SPARSE ? p.q_ptr[sg.r] : sg.q0;
+            q.n = SPARSE ? p.q_ptr[sg.r + 1] - q.q0 : sg.n;
+            q.p0 = sg.p0;
+            q.np = sg.np;
+            mass_rows = (size_t)q.n * g;
+            mass = mass_of(p, q, sg.h, false) + (SPARSE ? (sg.q0 - q.q0) * g : row0);
+        }
         // One turn: NG units, 16 tokens of each.  Two at a time hide each other's latencies (products in a
         // chain, conversions, the row maximum's shuffles): one warp alone keeps its scheduler a third busy.
         const auto turn = [&](auto groups) {
@@ -991,7 +998,6 @@ __global__ void __launch_bounds__(32 * kWeightWarps) cache_weight_kernel(const _
     const int u0 = run * kWeightTurns * (32 / S), u1 = min(p.c.total_pages, u0 + kWeightTurns * (32 / S));
     if (u0 >= p.c.total_pages) return;
     const int T = p.c.T, g = p.g, sub = lane & (S - 1);
-    const size_t rowsw = (size_t)p.max_q * g;
     // the lane's page and its request, looked up again only past the request's end
     int r = -1, end = -1;
     Request q{};
@@ -1015,9 +1021,11 @@ __global__ void __launch_bounds__(32 * kWeightWarps) cache_weight_kernel(const _
         float sum = 0.f;
         if (on && ok) {
             const int pg = u - q.p0;
-            const float2* src = p.ws_mass + ((size_t)q.p0 * p.c.Hkv + (size_t)h * q.np + pg) * (T / 16) * rowsw;
-            // the chunk kernel keeps one sum for each page and row, in the place of its first 16 tokens
-            const int rows = q.n * g, total = rows * (!SPARSE && rows >= p.big_rows ? 1 : T / 16);
+            // the chunk kernel keeps one sum for each page and row, the other one for every 16 tokens
+            const int rows = q.n * g;
+            const bool big = !SPARSE && rows >= p.big_rows;
+            const int total = rows * (big ? 1 : T / 16);
+            const float2* src = mass_of(p, q, h, big) + (size_t)pg * total;
             const uint32_t* bits = SPARSE ? p.ws_bits + (size_t)(q.p0 / 32 + r) * p.max_q * p.c.Hkv : nullptr;
             for (int e = pg * T < q.len ? sub : total; e < total; e += S) {
                 const int grp = e / rows, row = e - grp * rows, qi = row / g, j = row - qi * g;
@@ -1027,7 +1035,7 @@ __global__ void __launch_bounds__(32 * kWeightWarps) cache_weight_kernel(const _
                 if (pos >= q.len - q.n + qi + 1) continue;
                 if (SPARSE && !((bits[((size_t)qi * p.c.Hkv + h) * ((q.np + 31) / 32) + (pg >> 5)] >> (pg & 31)) & 1u))
                     continue;
-                const float2 a = src[(size_t)grp * rowsw + row];
+                const float2 a = src[e];
                 const float l2 = p.ws_lse[(size_t)(q.q0 + qi) * p.Hq + h * g + j];
                 // a row whose running maximum was still -inf has 0 here; NaN stays NaN
                 sum += a.x == 0.f ? 0.f : a.x * ex2((a.y == kNegInf ? 0.f : a.y - kOffset) - l2);

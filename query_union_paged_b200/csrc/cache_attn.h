@@ -41,7 +41,8 @@ struct CacheAttnParams {
     float* weight;    // page weights, or null
     float* part_o;    // [partial][row tile][128]: unnormalised sums, and in part_ml the log2 maximum
     float2* part_ml;  // they are relative to and the sum of weights
-    float2* ws_mass;  // page weights: per (16 tokens, row) the weights' sum and the maximum it is relative to
+    float2* mass;        // page weights: per (16 tokens, row) the weights' sum and the maximum it is relative to
+    float2* mass_chunk;  // and per (page, row) of the chunk kernel's requests; places by mass_of()
     float* ws_lse;    // page weights: log2-domain lse of every row
     uint32_t* ws_bits;  // page weights over TopK pages: the pages each (query, KV head) reads
     float* chunk_o;     // [2 per run][256][128], chunk_ml, spans [run]: the chunk kernel's partial results
@@ -54,6 +55,7 @@ struct CacheAttnParams {
     int Nq, max_q, Hq, g, Ksel;
     int per_units;   // all pages: least units of a CTA
     int max_tiles;   // all pages: row tiles of max_q queries
+    int mass_per, mass_chunk_per;  // rows of one request that a page has room for, 0: places by rows
     int nsplit;      // TopK pages: CTAs of one (query, KV head)
     int max_pages;   // pages of a request, at most
     int big_rows;    // all pages: requests of this many rows or more are the chunk kernel's
@@ -64,6 +66,15 @@ struct CacheAttnParams {
 __device__ __forceinline__ unsigned request_fault(const CacheAttnParams& p, const Request& q) {
     if (!q.ok || q.n > p.max_q) return QUP_ERR_GROUP;
     return q.np > p.max_pages ? QUP_ERR_CAPACITY : 0u;
+}
+// Page weights: the sums of request q's rows of KV head h, [page][T / 16, or 1 if big][n * g].  Requests lie
+// one behind the other either by their pages, with room for the longest one's rows, or by their rows, with room for
+// the most pages: what takes less for the whole batch.
+__device__ __forceinline__ float2* mass_of(const CacheAttnParams& p, const Request& q, int h, bool big) {
+    const int per = big ? p.mass_chunk_per : p.mass_per;
+    const size_t at = per ? ((size_t)q.p0 * p.c.Hkv + (size_t)h * q.np) * per
+                          : ((size_t)q.q0 * p.c.Hkv + (size_t)h * q.n) * p.g * p.max_pages;
+    return big ? p.mass_chunk + at : p.mass + at * (p.c.T / 16);
 }
 // Rows of faulty requests (`big`: those that would be the chunk kernel's) get O = 0 and lse = -inf: the CTAs
 // take the requests in turn.

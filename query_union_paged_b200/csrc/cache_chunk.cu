@@ -710,12 +710,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             float m = kNegInf, l = 0.f;
             const int b0 = sg.b0, b1 = sg.b1;
-            float2* mass_row = nullptr;  // page weights: this row's sums, rowsw * T / 16 apart per page
-            int mass_pages = 0;
+            float2* mass_row = nullptr;  // page weights: this row's sums, mass_rows apart
+            int mass_pages = 0, mass_rows = 0;
             if (WEIGHTS && on) {
-                const Request& q = wk.it.q;
-                mass_row = p.ws_mass + ((size_t)q.p0 * p.c.Hkv + (size_t)sg.h * q.np) * (T / 16) * ((size_t)p.max_q * g) + x;
-                mass_pages = (q.len + T - 1) / T;
+                mass_row = mass_of(p, wk.it.q, sg.h, true) + x;
+                mass_rows = wk.it.rows;
+                mass_pages = (wk.it.q.len + T - 1) / T;
             }
             for (int b = b0; b < b1; ++b, ++it) {
                 const uint32_t k = use++;
@@ -843,7 +843,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if ((t1 + 16) % T == 0) {
                             const int pg = b * PPS + t1 / T;
                             if (pg < mass_pages)
-                                mass_row[(size_t)pg * (T / 16) * ((size_t)p.max_q * g)] = make_float2(mass, m);
+                                mass_row[(size_t)pg * mass_rows] = make_float2(mass, m);
                             mass = 0.f;
                         }
                     }

@@ -7,7 +7,7 @@ import pytest
 
 import oracle.cache as oc
 import query_union_paged_b200 as qup
-from test_gpu_cache import Case, _bf16, _check_attn, _ptr, _run_attn
+from test_gpu_cache import Case, _bf16, _check_attn, _ptr, _run_attn, _topk
 
 pytestmark = pytest.mark.gpu
 
@@ -190,3 +190,39 @@ def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(ns, topk):
         assert code == qup.ERR["TIMEOUT"], (stage, code)
         got = qup.cache_attn(cache, q, ptr, max(ns), topk=tk, page_weight=w[1])
         assert qup.get_error() == 0 and torch.equal(got, want) and torch.equal(w[0], w[1]), stage
+
+
+# ------------------------------------------------------------------ page weights
+
+@pytest.mark.parametrize("lens,ns,topk", [
+    ([100, 900, 500], [40, 40, 40], False),                       # sums placed by pages, chunk kernel
+    ([300, 300, 290], [90, 33, 20], False),                       # by rows
+    ([500, 500, 500, 480], [1, 4, 1, 1], False),                  # by rows, small kernel
+    ([1500, 90, 200, 40], [1, 1, 1, 1], False),                   # by pages
+    ([1500, 90, 600, 1400, 33], [1, 70, 20, 2, 1], False),        # both kernels
+    ([500, 490, 500], [1, 6, 1], True),                           # TopK: by rows
+    ([700, 40, 500], [2, 2, 2], True),                            # and by pages
+])
+@pytest.mark.parametrize("T", [16, 64, 128])
+def test_page_weights_stay_in_their_workspace(T, lens, ns, topk):
+    """The smallest workspace that is reported, full of NaN, with a guard behind it: weights within their bound,
+    the guard untouched, the same bits with a workspace for any call."""
+    torch = _t()
+    c = Case(110 + T, lens, T=T)
+    g, N = 4, sum(ns)
+    tk = _topk(c, ns, g, 5, c.rng) if topk else None
+    o, lse, w, ref = _run_attn(c, ns, g, topk=tk, q=(q := 1.5 * c.rng.standard_normal((N, 8, 128))))
+    _check_attn(o, lse, w, ref, max(lens), (T, ns))
+    cache, ptr, qt = c.cache(), torch.from_numpy(_ptr(ns)).cuda(), _bf16(q)[1]
+    for kind in (topk, True):
+        size = qup.cache_attn_workspace(cache, N, 8, max(ns), page_weight=True, topk=kind).numel()
+        buf = torch.full((size + 4096,), 255, dtype=torch.uint8, device="cuda")
+        again = torch.empty(len(c.table), 2, device="cuda")
+        got = qup.cache_attn(cache, qt, ptr, max(ns), topk=None if tk is None else torch.from_numpy(tk).cuda(),
+                             page_weight=again, workspace=buf[:size])
+        assert qup.get_error() == 0 and torch.all(buf[size:] == 255)
+        assert np.array_equal(again.double().cpu().numpy(), w) and np.array_equal(got.double().cpu().numpy(), o)
+    small = qup.cache_attn_workspace(cache, N, 8, max(ns), page_weight=True, topk=topk)
+    with pytest.raises(qup.QupError):
+        qup.cache_attn(cache, qt, ptr, max(ns), topk=None if tk is None else torch.from_numpy(tk).cuda(),
+                       page_weight=again, workspace=small[:4 << 20])  # less than the smallest of all
