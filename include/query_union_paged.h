@@ -51,7 +51,7 @@ extern "C" {
 #define QUP_ERR_PHYS_PAGE 16   /* device: a page_table entry outside [0, P_phys) */
 #define QUP_ERR_GROUP 32       /* device: a group with no members, too many rows or a bad query ID */
 #define QUP_ERR_TIMEOUT 64     /* device: a pipeline wait exceeded its limit; the kernel exited cleanly */
-#define QUP_ERR_SCALE 128      /* device: a cache scale that is not finite, or a negative V scale */
+#define QUP_ERR_SCALE 128      /* device: a cache scale that is not finite, or a V scale out of range */
 
 /* dtype codes */
 #define QUP_F32 0
@@ -425,7 +425,9 @@ int qup_cache_append(const qup_cache* cache, const void* k_new, const void* v_ne
  * are request r's last positions, kv_len[r] - n .. kv_len[r] - 1; query i sees
  * the tokens t <= its position, of all pages or of the pages in its TopK rows:
  *   s_t = softmax_scale * (q . k_t) * k_scale,  O = sum softmax(s)_t v_t v_scale
- * KV head of Q head h' is h' / (Hq / Hkv).
+ * KV head of Q head h' is h' / (Hq / Hkv).  K scales are finite, V scales 0 or
+ * 2^-80 .. 2^80 (a V scale of 0 counts as 2^-64, what qup_cache_append gives a
+ * page of zeros).
  *   Q          device bf16 [Nq][Hq][128], q_stride elements from one query to
  *              the next (a multiple of 8, at least Hq * 128), 16-byte aligned
  *   max_q      queries of one request, at most

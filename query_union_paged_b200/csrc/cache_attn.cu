@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, cache_attn_ctas(NT))
                         } else {
                             ks = __ldg(p.c.k_scale + (size_t)phys * p.c.Hkv + sg.h);
                             const float vs = __ldg(p.c.v_scale + (size_t)phys * p.c.Hkv + sg.h);
-                            if (!(fabsf(ks) < INFINITY) || !(vs >= 0.f && vs < INFINITY)) {
+                            if (!(fabsf(ks) < INFINITY) || !v_scale_ok(vs)) {
                                 atomicOr(p.err, QUP_ERR_SCALE);
                                 phys = -1;
                             }

@@ -62,6 +62,12 @@ struct CacheAttnParams {
     int list_cap;    // TopK pages: distinct pages of one CTA, at most
 };
 
+// V scales that can be read: 0, or 2^-80 .. 2^80.  A row's sum adds up to p / vs with p <= 2^15 for each of fewer than
+// 2^31 tokens, and its largest p is at least 2^8: outside, the sum may pass fp32's range or lose what counts.
+__device__ __forceinline__ bool v_scale_ok(float vs) {
+    const uint32_t u = __float_as_uint(vs);
+    return (u << 1) == 0u || (u >= 0x17800000u && u <= 0x67800000u);
+}
 // What keeps a request from being read (0: nothing), as device error bits.
 __device__ __forceinline__ unsigned request_fault(const CacheAttnParams& p, const Request& q) {
     if (!q.ok || q.n > p.max_q) return QUP_ERR_GROUP;

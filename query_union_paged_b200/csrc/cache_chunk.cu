@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             } else {
                                 ks = __ldg(p.c.k_scale + (size_t)phys * p.c.Hkv + h);
                                 const float vs = __ldg(p.c.v_scale + (size_t)phys * p.c.Hkv + h);
-                                if (!(fabsf(ks) < INFINITY) || !(vs >= 0.f && vs < INFINITY)) {
+                                if (!(fabsf(ks) < INFINITY) || !v_scale_ok(vs)) {
                                     atomicOr(p.err, QUP_ERR_SCALE);
                                     phys = -1;
                                 }

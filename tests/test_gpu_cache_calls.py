@@ -89,6 +89,32 @@ def test_zero_and_tiny_query_rows_over_negative_scales():
     _check_attn(o, lse, w, ref, 200, "zero rows")
 
 
+@pytest.mark.parametrize("n", [2, 20])
+def test_v_scales_to_the_ends_of_their_range_and_past_them(n):
+    """V scales of 2^-80 and 2^80 are read as they are; past them a page is reported and not seen."""
+    torch = _t()
+    for k in (-80, 80):
+        c = Case(94 + k, [300, 70], T=64)
+        c.vs[:] = 2.0 ** k
+        o, lse, w, ref = _run_attn(c, [n, n], 4)
+        _check_attn(o, lse, w, ref, 300, k)
+    for bad in (2.0 ** -81, 1e-40, 2.0 ** 81, 3e38):
+        c = Case(95, [300, 70], T=64)
+        page = int(c.table[1])
+        good = c.vs[page].copy()
+        c.vs[page, 1] = bad
+        _, qt = _bf16(q := _bf16(c.rng.standard_normal((2 * n, 8, 128)))[0])
+        ptr = _ptr([n, n])
+        lse = torch.empty(2 * n, 8, device="cuda")
+        o = qup.cache_attn(c.cache(), qt, torch.from_numpy(ptr).cuda(), n, lse=lse)
+        assert qup.get_error() == qup.ERR["SCALE"], bad
+        c.vs[page] = good
+        topk = np.broadcast_to(np.arange(5, dtype=np.int32), (8, 2 * n, 5)).copy()
+        topk[4:, :n, 1] = -1  # request 0, KV head 1
+        ref = oc.attn(q, c.K, c.V, c.ks, c.vs, c.table, c.page_ptr, c.lens, ptr, 1 / math.sqrt(128), topk)
+        _check_attn(o.double().cpu().numpy(), lse.double().cpu().numpy(), None, ref, 300, bad)
+
+
 # ------------------------------------------------------------------ requests that contradict themselves
 
 def _faulty(c, ns, max_q, bad, g=4, lens=None, cut=0, topk=None, max_pages=None, code="GROUP"):
