@@ -381,7 +381,8 @@ int qup_page_major_attn(const void* Q, int q_dtype, const void* K_cache, const v
  *   page_ptr   device int32 [R+1], ascending; kv_len device int32 [R]: tokens
  *              of each request, at most its pages x T
  *   max_pages  page table entries of one request, at most (1 .. total_pages);
- *              attention and eviction refuse a request with more
+ *              attention refuses a request with more, eviction one with more
+ *              pages that hold tokens
  * Two requests may share physical pages for reading; pages that
  * qup_cache_append writes belong to one request.
  */
@@ -488,9 +489,12 @@ int qup_cache_attn(const qup_cache* cache, const void* Q, int64_t q_stride, cons
  *              other, but may be cache's own page_table and kv_len, and acc.  Entries of no request are left
  *              as they are.
  * Device errors: QUP_ERR_GROUP (contradictory request) and QUP_ERR_CAPACITY
- * (more than max_pages pages): the request's entries are copied unchanged.
- * QUP_ERR_ARG for max_pages beyond what one CTA's shared memory holds (24576).
+ * (more than max_pages pages with tokens): the request's entries are copied
+ * unchanged.  QUP_ERR_ARG for max_pages above QUP_CACHE_EVICT_PAGES, which one
+ * CTA's shared memory holds: for a longer table with shorter requests give
+ * that.
  */
+#define QUP_CACHE_EVICT_PAGES 24576
 int qup_cache_evict(const qup_cache* cache, const float* page_weight, const float* acc, float decay, int budget,
                     int sink, int recent, int32_t* table_out, float* acc_out, int32_t* len_out, int32_t* page_src,
                     void* stream);

@@ -30,10 +30,12 @@ import numpy as np
 
 __all__ = ["Groups", "sparse_group", "sparse_prefill_attn", "build_bundles", "groups_from_host", "union_support",
            "Batch", "batch_prepare", "sparse_prefill_attn_batch", "PageItems", "page_major_items", "page_major_attn",
-           "KVCache", "cache_append", "cache_attn", "cache_attn_workspace", "cache_evict", "get_error", "set_debug", "set_checked", "load",
-           "QupError", "F32", "BF16", "E4M3", "ERR"]
+           "KVCache", "cache_append", "cache_attn", "cache_attn_workspace", "cache_evict", "get_error", "set_debug",
+           "set_checked", "load",
+           "QupError", "F32", "BF16", "E4M3", "EVICT_PAGES", "ERR"]
 
 F32, BF16, E4M3 = 0, 1, 2
+EVICT_PAGES = 24576  # QUP_CACHE_EVICT_PAGES
 ERR = {"ARG": 1, "CAPACITY": 2, "CUDA": 4, "PAGE_ID": 8, "PHYS_PAGE": 16, "GROUP": 32, "TIMEOUT": 64,
        "SCALE": 128}
 
@@ -491,14 +493,15 @@ class KVCache:
     K, V [P_phys][Hkv][T][128] uint8 or float8_e4m3fn; k_scale, v_scale fp32 [P_phys][Hkv];
     page_table int32 [total_pages], request r's logical pages being the entries
     page_ptr[r] .. page_ptr[r+1); page_ptr int32 [R+1]; kv_len int32 [R], the tokens of each request.
-    max_pages: page table entries of one request, at most (default: all of them).
+    max_pages: page table entries of one request, at most (default: all of them, and for cache_evict
+    EVICT_PAGES pages with tokens, if that is less).
 
     The object keeps the tensors and passes their addresses: their contents may change (kv_len grows,
     the page table is rewritten by cache_evict), the tensors may not be replaced.
     """
 
     __slots__ = ("K", "V", "k_scale", "v_scale", "page_table", "page_ptr", "kv_len", "max_pages", "device", "R", "Hkv",
-                 "total_pages", "_c", "_ref", "_index")
+                 "total_pages", "_c", "_ref", "_evict_c", "_evict_ref", "_index")
 
     def __init__(self, K, V, k_scale, v_scale, page_table, page_ptr, kv_len, max_pages: Optional[int] = None):
         import torch
@@ -515,7 +518,8 @@ class KVCache:
         _need(page_ptr.numel() == kv_len.numel() + 1, "page_ptr has one entry more than kv_len")
         _need(T in (16, 32, 64, 128), f"page size {T}: 16, 32, 64 or 128 wanted")
         _need(page_table.numel() > 0 and P_phys > 0, "an empty page table or cache")
-        if max_pages is None:
+        given = max_pages is not None
+        if not given:
             max_pages = page_table.numel()
         _need(1 <= max_pages <= page_table.numel(), f"max_pages {max_pages}: 1 .. {page_table.numel()} wanted")
         _need(K.is_cuda, f"the cache is on {K.device}: CUDA tensors wanted")
@@ -525,7 +529,11 @@ class KVCache:
         self.R, self.Hkv, self.total_pages = kv_len.numel(), Hkv, page_table.numel()
         self._c = _CacheStruct(*[t.data_ptr() for t in (K, V, k_scale, v_scale, page_table, page_ptr, kv_len)],
                                P_phys, Hkv, T, self.R, self.total_pages, max_pages)
-        self._ref = ctypes.byref(self._c)
+        self._ref = self._evict_ref = ctypes.byref(self._c)
+        if not given and max_pages > EVICT_PAGES:  # no limit was given: eviction's own
+            self._evict_c = _CacheStruct.from_buffer_copy(self._c)
+            self._evict_c.max_pages = EVICT_PAGES
+            self._evict_ref = ctypes.byref(self._evict_c)
 
 
 def _made_on(stream):
@@ -654,7 +662,7 @@ def cache_evict(cache: KVCache, page_weight, acc, budget: int, sink: int = 1, re
     _whole(acc_out, "out acc", torch.float32, (n,), index)
     _whole(lens, "out kv_len", torch.int32, (cache.R,), index)
     _whole(src, "out page_src", torch.int32, (n,), index)
-    _launch((_lib or load()).qup_cache_evict, "qup_cache_evict", index, stream, cache._ref, page_weight.data_ptr(),
+    _launch((_lib or load()).qup_cache_evict, "qup_cache_evict", index, stream, cache._evict_ref, page_weight.data_ptr(),
             acc.data_ptr(), decay, budget, sink, recent, table.data_ptr(), acc_out.data_ptr(), lens.data_ptr(),
             src.data_ptr())
     return table, acc_out, lens, src

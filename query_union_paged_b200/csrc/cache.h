@@ -61,8 +61,7 @@ cudaError_t launch_cache_append(const CacheView& c, const void* k_new, const voi
                                 long long k_stride, long long v_stride, const int32_t* tok_ptr, int N, int sms,
                                 unsigned* err, cudaStream_t stream);
 
-// At most kMaxEvictPages used pages of one request (a CTA's shared memory holds them).
-constexpr int kMaxEvictPages = 24576;
+// cap: used pages of one request, at most (QUP_CACHE_EVICT_PAGES: a CTA's shared memory holds them)
 size_t cache_evict_smem(int cap);
 cudaError_t launch_cache_evict(const CacheView& c, const float* weight, const float* acc, float decay, int budget,
                                int sink, int recent, int cap, int32_t* table_out, float* acc_out, int32_t* len_out,

@@ -283,7 +283,7 @@ int qup_cache_evict(const qup_cache* cache, const float* page_weight, const floa
     int rc = check_cache(cache);
     if (rc) return rc;
     if (!std::isfinite(decay) || budget < 1 || sink < 0 || recent < 1) return QUP_ERR_ARG;
-    if (cache->max_pages > qup::kMaxEvictPages) return QUP_ERR_ARG;
+    if (cache->max_pages > QUP_CACHE_EVICT_PAGES) return QUP_ERR_ARG;
     if (cache->R == 0) return QUP_OK;
     if (!cache->page_table || !cache->page_ptr || !cache->kv_len || !page_weight || !acc || !table_out || !acc_out ||
         !len_out || !page_src)

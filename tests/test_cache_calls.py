@@ -30,3 +30,13 @@ def test_workspace_of_page_weights_follows_the_rows_and_pages_that_exist():
     # sizes whose product passes 64 bits
     assert size(1, 128, 1, 1 << 23, 1 << 30, 1 << 30, 1 << 27) >= 1 << 62
 """)
+
+
+def test_eviction_limit_is_the_headers():
+    import os
+    import re
+
+    import query_union_paged_b200 as qup
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = open(os.path.join(root, "include", "query_union_paged.h")).read()
+    assert int(re.search(r"#define QUP_CACHE_EVICT_PAGES (\d+)", text).group(1)) == qup.EVICT_PAGES

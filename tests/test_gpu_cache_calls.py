@@ -189,6 +189,32 @@ def test_no_queries_of_any_request():
         assert torch.all(o[2] == 5) and torch.all(w == 0)
 
 
+# ------------------------------------------------------------------ arguments
+
+def test_a_long_page_table_of_short_requests_is_evicted():
+    """Without max_pages a table longer than one request's limit is no error; a request past the limit is."""
+    torch = _t()
+    rng = np.random.default_rng(101)
+    lens, pages = np.array([150, 90, 24600 * 16], np.int32), [12, 9, 24610]
+    ptr = np.concatenate([[0], np.cumsum(pages)]).astype(np.int32)
+    n = 30000
+    table = rng.permutation(n).astype(np.int32)
+    dev = lambda a: torch.from_numpy(a).cuda()
+    kv = torch.zeros(1, 1, 16, 128, dtype=torch.uint8, device="cuda")
+    one = torch.ones(1, 1, device="cuda")
+    make = lambda **kw: qup.KVCache(kv, kv, one, one, dev(table), dev(ptr), dev(lens), **kw)
+    acc, w = rng.random(n).astype(np.float32), rng.random((n, 1)).astype(np.float32)
+    got = qup.cache_evict(make(), dev(w), dev(acc), 4)
+    assert qup.get_error() == qup.ERR["CAPACITY"]
+    want = oc.evict(table, acc, w, ptr[:3], lens[:2], 16, 4, 1, 1, 1.0)
+    m = int(ptr[2])
+    for a, b in zip((got[0][:m], got[1][:m], got[2][:2], got[3][:m]), (want[0][:m], want[1][:m], want[2], want[3][:m])):
+        assert np.array_equal(a.cpu().numpy(), b)
+    assert np.array_equal(got[0][m:ptr[3]].cpu().numpy(), table[m:ptr[3]]) and int(got[2][2]) == lens[2]
+    with pytest.raises(qup.QupError):  # a limit that the caller gives is taken at its word
+        qup.cache_evict(make(max_pages=n), dev(w), dev(acc), 4)
+
+
 # ------------------------------------------------------------------ waits that run out
 
 @pytest.mark.parametrize("ns,topk", [([1, 1, 1], None), ([4, 4, 2], None), ([40, 40, 40], None), ([70, 1, 3], None),
