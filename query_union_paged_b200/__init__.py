@@ -469,6 +469,12 @@ def _need(ok, what: str):
         raise ValueError(what)
 
 
+def _int32(**numbers):
+    """The numbers fit the C call's int (ctypes would cut them without a word)."""
+    for name, x in numbers.items():
+        _need(-1 << 31 <= x < 1 << 31, f"{name} {x}: out of 32 bits")
+
+
 def _whole(t, name: str, dtype, shape, index: int):
     """t is a contiguous tensor of this type and shape on device `index`.  The message is put together only
     when it is needed: these checks are most of what a short call costs on the host."""
@@ -588,6 +594,7 @@ def cache_attn_workspace(cache: KVCache, Nq: int, Hq: int, max_q: int, page_weig
     for calls without topk only: up to T / 16 times smaller where requests are long.
     """
     import torch
+    _int32(Nq=Nq, Hq=Hq, max_q=max_q)
     n = ctypes.c_size_t(0)
     _check(load().qup_cache_attn_workspace(cache._ref, Nq, max_q, Hq, (1 if topk else 2) if page_weight else 0,
                                            ctypes.byref(n)), "qup_cache_attn_workspace")
@@ -608,6 +615,7 @@ def cache_attn(cache: KVCache, Q, q_ptr, max_q: int, topk=None, softmax_scale: O
     index = cache._index
     _need(Q.dim() == 3, "Q: [Nq][Hq][128] wanted")
     Nq, Hq, _ = shape = Q.shape
+    _int32(max_q=max_q)
     _heads(Q, "Q", torch.bfloat16, (Nq, Hq, 128), index)
     _whole(q_ptr, "q_ptr", torch.int32, (cache.R + 1,), index)
     ksel = topk_p = lse_p = weight_p = None
@@ -651,6 +659,7 @@ def cache_evict(cache: KVCache, page_weight, acc, budget: int, sink: int = 1, re
     """
     import torch
     index, n = cache._index, cache.total_pages
+    _int32(budget=budget, sink=sink, recent=recent)
     _whole(page_weight, "page_weight", torch.float32, (n, cache.Hkv), index)
     _whole(acc, "acc", torch.float32, (n,), index)
     if out is None:

@@ -215,6 +215,25 @@ def test_a_long_page_table_of_short_requests_is_evicted():
         qup.cache_evict(make(max_pages=n), dev(w), dev(acc), 4)
 
 
+def test_numbers_past_32_bits_are_refused():
+    torch = _t()
+    c = Case(102, [100, 40], T=16)
+    cache, n = c.cache(), len(c.table)
+    _, qt = _bf16(c.rng.standard_normal((2, 8, 128)))
+    ptr = torch.arange(3, dtype=torch.int32, device="cuda")
+    w, acc = torch.rand(n, 2, device="cuda"), torch.rand(n, device="cuda")
+    for big in (1 << 31, 1 << 32, (1 << 32) + 1, 1 << 63, -(1 << 32) + 1):
+        for kw in (dict(budget=big), dict(sink=big), dict(recent=big)):
+            with pytest.raises(ValueError):
+                qup.cache_evict(cache, w, acc, **{**dict(budget=3), **kw})
+        with pytest.raises(ValueError):
+            qup.cache_attn(cache, qt, ptr, big)
+        for sizes in ((big, 8, 1), (2, big, 1), (2, 8, big)):
+            with pytest.raises(ValueError):
+                qup.cache_attn_workspace(cache, *sizes)
+    assert qup.get_error() == 0
+
+
 # ------------------------------------------------------------------ waits that run out
 
 @pytest.mark.parametrize("ns,topk", [([1, 1, 1], None), ([4, 4, 2], None), ([40, 40, 40], None), ([70, 1, 3], None),
