@@ -412,6 +412,7 @@ typedef struct {
  *             (bf16) or 4 (fp32) and at least Hkv * 128; the pointers are
  *             16-byte aligned (heads and elements are contiguous)
  *   tok_ptr   device int32 [R+1], ascending; rows of no request are not read
+ * K and V, and their scales, are tensors of their own (QUP_ERR_ARG).
  * Device errors: QUP_ERR_GROUP for a request whose rows, length and pages
  * contradict each other (nothing of it is written), QUP_ERR_PHYS_PAGE for a
  * page_table entry out of range, QUP_ERR_SCALE for an old scale that is
@@ -436,8 +437,9 @@ int qup_cache_append(const qup_cache* cache, const void* k_new, const void* v_ne
  *              request, -1 = padding (duplicates count once), or NULL for all
  *              pages (Ksel = 0 with a pointer selects none); Hq / Hkv <= 32 with
  *              topk
- *   O          device bf16 [Nq][Hq][128], 16-byte aligned, apart from Q; rows
- *              of no request are not written; a row that sees nothing gets 0
+ *   O          device bf16 [Nq][Hq][128], 16-byte aligned, apart from Q's rows
+ *              (QUP_ERR_ARG); rows of no request are not written; a row that
+ *              sees nothing gets 0
  *   lse        device fp32 [Nq][Hq] natural-log sum of exponentials (-inf for a
  *              row that sees nothing), or NULL
  *   page_weight device fp32 [total_pages][Hkv] or NULL: the softmax weight that
@@ -486,8 +488,9 @@ int qup_cache_attn(const qup_cache* cache, const void* Q, int64_t q_stride, cons
  *              pages, acc for unused entries); len_out device int32 [R], the
  *              new kv_len; page_src device int32 [total_pages], the old
  *              request-local place of each entry.  They are apart from each
- *              other, but may be cache's own page_table and kv_len, and acc.  Entries of no request are left
- *              as they are.
+ *              other and from the inputs (QUP_ERR_ARG), but table_out, len_out
+ *              and acc_out may be cache's own page_table and kv_len, and acc.
+ *              Entries of no request are left as they are.
  * Device errors: QUP_ERR_GROUP (contradictory request) and QUP_ERR_CAPACITY
  * (more than max_pages pages with tokens): the request's entries are copied
  * unchanged.  QUP_ERR_ARG for max_pages above QUP_CACHE_EVICT_PAGES, which one

@@ -47,6 +47,17 @@ qup::CacheView view_of(const qup_cache* c) {
     return v;
 }
 
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+// The rows of Q (`row` bytes each, `stride` apart) against n contiguous rows of O.
+bool rows_overlap(const void* Q, int64_t stride, const void* O, int64_t row, int64_t n) {
+    const int64_t at = (int64_t)(reinterpret_cast<intptr_t>(O) - reinterpret_cast<intptr_t>(Q));
+    const int64_t first = at < row ? 0 : (at - row) / stride + 1;  // the first row of Q that ends behind O's start
+    return first < n && first * stride < at + row * n;
+}
+
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // All pages: requests of up to kCacheSmallRows rows (queries x heads of a KV head) go to the kernel
@@ -137,6 +148,7 @@ int qup_cache_append(const qup_cache* cache, const void* k_new, const void* v_ne
     if (N == 0 || cache->R == 0) return QUP_OK;
     if (check_cache_pointers(cache) || !k_new || !v_new || !tok_ptr) return QUP_ERR_ARG;
     if ((reinterpret_cast<uintptr_t>(k_new) | reinterpret_cast<uintptr_t>(v_new)) & 15) return QUP_ERR_ARG;
+    if (cache->K == cache->V || cache->k_scale == cache->v_scale) return QUP_ERR_ARG;  // both are written
     if (((int64_t)N / cache->T + 2 * (int64_t)cache->R) * 2 * cache->Hkv >= ((int64_t)1 << 31)) return QUP_ERR_ARG;
     qup::DeviceInfo dev;
     if ((rc = qup::device_info(&dev))) return rc;
@@ -181,7 +193,8 @@ int qup_cache_attn(const qup_cache* cache, const void* Q, int64_t q_stride, cons
     if (check_cache_pointers(cache) || !Q || !q_ptr || !O || !ws) return QUP_ERR_ARG;
     if ((reinterpret_cast<uintptr_t>(Q) | reinterpret_cast<uintptr_t>(O) | reinterpret_cast<uintptr_t>(ws)) & 15)
         return QUP_ERR_ARG;
-    if (O == Q) return QUP_ERR_ARG;  // rows of Q are read after others of O are written
+    // rows of Q are read after others of O are written
+    if (rows_overlap(Q, 2 * q_stride, O, (int64_t)Hq * d * 2, Nq)) return QUP_ERR_ARG;
     const AttnWs L = attn_ws_layout(cache, Nq, max_q, Hq, page_weight != nullptr, sparse);
     if (ws_bytes < L.total) return QUP_ERR_CAPACITY;
 
@@ -288,6 +301,26 @@ int qup_cache_evict(const qup_cache* cache, const float* page_weight, const floa
     if (!cache->page_table || !cache->page_ptr || !cache->kv_len || !page_weight || !acc || !table_out || !acc_out ||
         !len_out || !page_src)
         return QUP_ERR_ARG;
+    // a request's entries are read before its own are written, others' perhaps after: an output may be the input of the
+    // same layout and nothing else
+    const size_t n = sizeof(int32_t) * (size_t)cache->total_pages, nr = sizeof(int32_t) * (size_t)cache->R;
+    const struct {
+        const void* p;
+        size_t bytes;
+        const void* same;
+    } outs[4] = {{table_out, n, cache->page_table}, {acc_out, n, acc}, {len_out, nr, cache->kv_len}, {page_src, n, nullptr}},
+      ins[5] = {{cache->page_table, n, nullptr},
+                {acc, n, nullptr},
+                {cache->kv_len, nr, nullptr},
+                {cache->page_ptr, nr + sizeof(int32_t), nullptr},
+                {page_weight, n * cache->Hkv, nullptr}};
+    for (int i = 0; i < 4; ++i) {
+        for (int j = 0; j < i; ++j)
+            if (overlap(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes)) return QUP_ERR_ARG;
+        for (const auto& in : ins)
+            if (!(outs[i].p == in.p && in.p == outs[i].same) && overlap(outs[i].p, outs[i].bytes, in.p, in.bytes))
+                return QUP_ERR_ARG;
+    }
     qup::DeviceInfo dev;
     if ((rc = qup::device_info(&dev))) return rc;
     return qup::launch_cache_evict(view_of(cache), page_weight, acc, decay, budget, sink, recent, cache->max_pages,

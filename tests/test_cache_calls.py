@@ -40,3 +40,44 @@ def test_eviction_limit_is_the_headers():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     text = open(os.path.join(root, "include", "query_union_paged.h")).read()
     assert int(re.search(r"#define QUP_CACHE_EVICT_PAGES (\d+)", text).group(1)) == qup.EVICT_PAGES
+
+
+def test_outputs_over_inputs_or_each_other_are_refused():
+    _run_without_devices(_CACHE + """
+    V = ctypes.c_void_p
+    ws = ctypes.c_size_t(0)
+    c = cache(total_pages=30, R=3)
+    lib.qup_cache_attn_workspace(ctypes.byref(c), 5, 3, 32, 0, ctypes.byref(ws))
+    def attn(q, o, stride=4096, Nq=5):
+        return lib.qup_cache_attn(ctypes.byref(c), V(q), stride, A[1], Nq, min(3, Nq), 32, 128, None, 0, 0.1, V(o), None,
+                                  None, A[3], ws.value, None)
+    q, row = 0x400000, 8192
+    for o in (q, q + row, q + 4 * row, q + 5 * row - 16, q - row, q - 5 * row + 16, q + 16):
+        assert attn(q, o) == ARG, o - q
+    for o in (q + 5 * row, q - 5 * row):
+        assert attn(q, o) == NODEV, o - q
+    # Q as columns of a wider buffer of three rows' width: O may lie between two rows only where it fits
+    wide = 3 * 4096
+    for o in (q + 16, q + 2 * 3 * row, q + 4 * 3 * row, q + row, q - 5 * row + 16, q + 4 * 3 * row + row - 16):
+        assert attn(q, o, wide) == ARG, o - q
+    assert attn(q, q + row, wide, Nq=1) == NODEV and attn(q, q + 2 * row, wide, Nq=1) == NODEV
+    assert attn(q, q + row, wide, Nq=2) == NODEV and attn(q, q + 2 * row, wide, Nq=2) == ARG
+    assert attn(q, q + 4 * 3 * row + row, wide) == NODEV
+
+    own = dict(table=c.page_table, acc=0x600000, lens=c.kv_len, src=0x700000, ptr=c.page_ptr, w=0x800000)
+    def evict(table=0x610000, acc=0x620000, lens=0x630000, src=0x700000):
+        return lib.qup_cache_evict(ctypes.byref(c), V(own["w"]), V(own["acc"]), 0.9, 8, 1, 1, V(table), V(acc), V(lens),
+                                   V(src), None)
+    assert evict() == NODEV
+    assert evict(own["table"], own["acc"], own["lens"]) == NODEV  # in place
+    for kw in (dict(table=own["acc"]), dict(acc=own["table"]), dict(src=own["table"]), dict(lens=own["ptr"]),
+               dict(src=own["w"] + 956), dict(acc=own["w"]), dict(lens=own["table"]), dict(acc=own["acc"] + 4),
+               dict(table=own["table"] + 8), dict(lens=own["lens"] - 8), dict(src=own["lens"]), dict(table=own["ptr"]),
+               dict(table=0x700000), dict(acc=0x610000), dict(lens=0x700000 + 116), dict(acc=0x700000 - 116)):
+        assert evict(**kw) == ARG, kw
+    assert evict(src=own["w"] + 960) == NODEV and evict(acc=0x700000 - 120) == NODEV
+    for kw in (dict(V=0x1000000), dict(v_scale=0x1020000)):
+        bad = cache(**kw)
+        assert bad.K == bad.V or bad.k_scale == bad.v_scale
+        assert lib.qup_cache_append(ctypes.byref(bad), A[0], A[1], 1, 1024, 1024, A[2], 5, 128, None) == ARG, kw
+""")
