@@ -430,6 +430,15 @@ int qup_cache_append(const qup_cache* cache, const void* k_new, const void* v_ne
  * KV head of Q head h' is h' / (Hq / Hkv).  K scales are finite, V scales 0 or
  * 2^-80 .. 2^80 (a V scale of 0 counts as 2^-64, what qup_cache_append gives a
  * page of zeros).
+ * The products' roundings: the weights that multiply V are held in fp16 (2^-11)
+ * relative to the row's largest softmax weight x V scale, so beside that each
+ * token may be off by 2^-33 * 448 * the largest V scale of the pages that the
+ * row sees: one page whose scale an outlier made larger than the others' by
+ * 2^22 or more costs those bits, also where the outlier itself is not seen.  A
+ * token's part in the sum of weights, lse and page_weight is lost below 2^-134 *
+ * that scale / its own page's.  For requests of more than 16 rows of a KV head Q
+ * is held exactly down to 2^-9 of the row's largest element and within 2^-17
+ * of it below.  Sums are fp32.
  *   Q          device bf16 [Nq][Hq][128], q_stride elements from one query to
  *              the next (a multiple of 8, at least Hq * 128), 16-byte aligned
  *   max_q      queries of one request, at most

@@ -115,6 +115,23 @@ def test_v_scales_to_the_ends_of_their_range_and_past_them(n):
         _check_attn(o.double().cpu().numpy(), lse.double().cpu().numpy(), None, ref, 300, bad)
 
 
+@pytest.mark.parametrize("n", [2, 30])
+@pytest.mark.parametrize("octaves", [16, 24, 30])
+def test_a_page_whose_scale_an_unseen_token_made_large(n, octaves):
+    """The header's bound where one page's V scale is far above the values that the row sees of it: each
+    token may be off by 2^-33 * 448 * the largest V scale of the row's pages."""
+    c = Case(96, [200, 150], T=64)
+    for r in range(2):
+        last = c.table[c.page_ptr[r] + (c.lens[r] - 1) // 64]
+        c.vs[last] *= 2.0 ** octaves
+        c.V[last, :, :(c.lens[r] - 1) % 64] = 0x01  # 2^-9 but for the last token, which the last query alone sees
+    o, lse, w, ref = _run_attn(c, [n, n], 4)
+    for r in range(2):
+        top = c.vs[c.table[c.page_ptr[r]:c.page_ptr[r] + (c.lens[r] + 63) // 64]].max(axis=0)
+        ref["vtop"][r * n:(r + 1) * n] = 448.0 * np.repeat(top, 4)
+    _check_attn(o, lse, w, ref, 200, (n, octaves))
+
+
 # ------------------------------------------------------------------ requests that contradict themselves
 
 def _faulty(c, ns, max_q, bad, g=4, lens=None, cut=0, topk=None, max_pages=None, code="GROUP"):
