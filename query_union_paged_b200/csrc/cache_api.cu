@@ -224,7 +224,7 @@ int qup_cache_attn(const qup_cache* cache, const void* Q, int64_t q_stride, cons
         const int64_t entries = std::min<int64_t>((int64_t)g * Ksel, c.max_pages);
         const int64_t units = std::max<int64_t>((entries * c.T + qup::kCacheUnit - 1) / qup::kCacheUnit, 1);
         // as many CTAs as the SMs hold at once: finding its pages costs a CTA what 8 units do, so more
-        // and shorter ones lose (32 x 32K, 32 of 64-token pages: 41 us with one CTA a pair, 55 with four)
+        // and shorter ones lose (32 x 32K, 32 of 64-token pages: 35 us with one CTA a pair, 53 with four)
         p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>(ctas / items, units));
         p.list_cap = (int)((entries + p.nsplit - 1) / p.nsplit);
         grid = (int)(items * p.nsplit);
@@ -280,7 +280,6 @@ int qup_cache_attn(const qup_cache* cache, const void* Q, int64_t q_stride, cons
     p.Hq = Hq;
     p.g = g;
     p.Ksel = Ksel;
-    p.per_units = 1;
     p.max_pages = c.max_pages;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (chunk && qup::launch_cache_chunk(tmc[0], tmc[1], p, std::min(dev.sms, qup::kChunkMaxRuns), st) != cudaSuccess)

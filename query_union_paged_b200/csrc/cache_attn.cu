@@ -28,8 +28,8 @@
 // (query, KV head), its distinct pages cut into an equal share per CTA.
 //
 // Bound by DRAM: 2 * 128 bytes per token and KV head.  16 requests of 33K to 64K tokens, 8 KV heads, 32
-// heads: 264 us, 6.0 TB/s (0.91 of a copy); a TopK call of 32 pages of 64 tokens 41 us, 3.3 TB/s (finding a
-// query's pages costs a CTA about 5 us before its first load).
+// heads: 265 to 280 us, 5.7 to 6.0 TB/s (0.86 to 0.91 of a copy); a TopK call of 32 pages of 64 tokens 35 us,
+// 3.8 TB/s (finding a query's pages costs a CTA about 5 us before its first load).
 #include <algorithm>
 #include <cstdint>
 #include <type_traits>
@@ -63,17 +63,6 @@ struct PageMeta {
     int pad[3];
 };
 
-// four E4M3 values to two pairs of fp16
-__device__ __forceinline__ void cvt_e4m3x4(uint32_t v, uint32_t& lo, uint32_t& hi) {
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(v));
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t* a, uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -90,16 +79,6 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
     return v;
 }
-__device__ __forceinline__ float lg2(float x) {
-    float y;
-    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ bool has_nan_byte(uint32_t w) {  // an E4M3 NaN (0x7f or 0xff) among four
-    const uint32_t x = (w & 0x7f7f7f7fu) + 0x01010101u;
-    return (x & 0x80808080u) != 0u;
-}
-
 // A bounded wait that the warp's lanes answer as one: a lane whose own limit had run out would leave the
 // others in shuffles, votes and products of the whole warp.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
@@ -111,8 +90,7 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 __device__ __forceinline__ int units_of(int len) { return (len + kUnit - 1) / kUnit; }
 __device__ __forceinline__ int tiles_of(int n, int g, int RT) { return (n * g + RT - 1) / RT; }
 
-// The requests' unit counts added up: this thread's sum over its own consecutive requests, then the
-// CTA's exclusive prefix (in `part`, kThreads entries).  total in *all.
+// A thread's own consecutive requests: their unit counts are added up, and the sums over the CTA.
 struct Span {
     int r0, r1;
 };
@@ -152,8 +130,8 @@ __device__ __forceinline__ long long cta_prefix(long long v, long long* part, lo
 }
 
 // Units of one CTA's run: an equal share of all of them.
-__device__ __forceinline__ int units_per_cta(const CacheAttnParams& p, long long all, int grid) {
-    return max(p.per_units, (int)((all + grid - 1) / grid));
+__device__ __forceinline__ int units_per_cta(long long all, int grid) {
+    return max(1, (int)((all + grid - 1) / grid));
 }
 
 // Where a CTA's run of units begins, and how long it is.
@@ -281,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, cache_attn_ctas(NT))
         if (bad) atomicOr(p.err, bad);
         long long all = 0;
         const long long mine = cta_prefix(sum, scan, &all);
-        const int per = units_per_cta(p, all, (int)gridDim.x);
+        const int per = units_per_cta(all, (int)gridDim.x);
         const long long u0 = (long long)blockIdx.x * per;
         if (u0 < all) {
             if (u0 >= mine && u0 < mine + sum) {
@@ -708,8 +686,7 @@ __global__ void __launch_bounds__(kThreads, cache_attn_ctas(NT))
                         for (int e = 0; e < 4; ++e) {
                             if (!live[n] || pos[n] + 2 * q4 + (e & 1) + 8 * (e >> 1) >= vis_any)
                                 v[e][0] = v[e][1] = v[e][2] = v[e][3] = 0u;
-                            nan = nan || has_nan_byte(v[e][0]) || has_nan_byte(v[e][1]) || has_nan_byte(v[e][2]) ||
-                                  has_nan_byte(v[e][3]);
+                            nan = nan || (nan_bytes(v[e][0]) | nan_bytes(v[e][1]) | nan_bytes(v[e][2]) | nan_bytes(v[e][3])) != 0u;
                         }
                         slow = __any_sync(0xffffffffu, nan);
                     }
@@ -965,7 +942,7 @@ __global__ void __launch_bounds__(kHeadDim) cache_merge_kernel(const __grid_cons
                 sum += red[0][y];
                 upto += red[1][y];
             }
-            const int per = units_per_cta(p, sum, grid_x);
+            const int per = units_per_cta(sum, grid_x);
             const long long a = upto + (h * nt + tile) * nb;  // the item's first unit
             c0 = (int)(a / per);
             nc = (int)((a + nvis - 1) / per) - c0 + 1;

@@ -1,5 +1,5 @@
-// cache_attn.h -- parameters and launchers of attention over the 8-bit page-scaled cache
-// (cache_attn.cu), for the C ABI (cache_api.cu).
+// cache_attn.h -- attention over the 8-bit page-scaled cache: parameters and launchers for the C ABI
+// (cache_api.cu), and what its two kernels (cache_attn.cu, cache_chunk.cu) have in common.
 #pragma once
 #include <cstddef>
 #include <cstdint>
@@ -53,7 +53,6 @@ struct CacheAttnParams {
     int dbg_skip_stage;  // a stage of each CTA that is not loaded, so that its waits run out; -1: none
     float scale_log2;
     int Nq, max_q, Hq, g, Ksel;
-    int per_units;   // all pages: least units of a CTA
     int max_tiles;   // all pages: row tiles of max_q queries
     int mass_per, mass_chunk_per;  // rows of one request that a page has room for, 0: places by rows
     int nsplit;      // TopK pages: CTAs of one (query, KV head)
@@ -61,6 +60,26 @@ struct CacheAttnParams {
     int big_rows;    // all pages: requests of this many rows or more are the chunk kernel's
     int list_cap;    // TopK pages: distinct pages of one CTA, at most
 };
+
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// four E4M3 values to two pairs of fp16
+__device__ __forceinline__ void cvt_e4m3x4(uint32_t v, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(v));
+}
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {  // 0x80 at each E4M3 NaN (0x7f, 0xff)
+    return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
 
 // V scales that can be read: 0, or 2^-80 .. 2^80.  A row's sum adds up to p / vs with p <= 2^15 for each of fewer than
 // 2^31 tokens, and its largest p is at least 2^8: outside, the sum may pass fp32's range or lose what counts.

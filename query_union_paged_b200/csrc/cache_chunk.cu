@@ -28,7 +28,7 @@
 // Bound: a step of 256 rows takes about 4,600 cycles.  The two warpgroups' softmax takes 2,500 to 3,200 of
 // them together (their exponentials alone 1,800 to 2,100, of which the MUFU unit 1,790), the tensor
 // cores 2,050; what does not overlap is the way from P to the next S (O update, S, two completions of
-// 200 to 400 cycles each).  1,024 queries x 32 heads behind 16K tokens: 335 us, 0.85 PFLOP/s.
+// 200 to 400 cycles each).  1,024 queries x 32 heads behind 16K tokens: 335 to 340 us, 0.84 PFLOP/s.
 // Measured and left out: loops unrolled over a step (instruction fetch: +23 %), the warpgroups taking
 // turns (+57 %: one alone is hardly faster than both together), half steps with S, P and O update of their
 // own (+14 %: products of 64 columns take as long to issue as of 128), a step's tokens split over both
@@ -91,22 +91,6 @@ struct Layout {
     static constexpr uint32_t total = walks + (kThreads / 32) * 128;
 };
 
-__device__ __forceinline__ float lg2(float x) {
-    float y;
-    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-// four E4M3 values to two pairs of fp16
-__device__ __forceinline__ void cvt_e4m3x4(uint32_t v, uint32_t& lo, uint32_t& hi) {
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(v));
-}
 __device__ __forceinline__ void f16x2_to_f32(uint32_t v, float& lo, float& hi) {
     asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
         : "=f"(lo), "=f"(hi)
@@ -117,10 +101,6 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {  // NaN i
     asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
     return y;
 }
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {  // 0x80 at each E4M3 NaN (0x7f, 0xff)
-    return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-}
-
 // sum over t in [0, n) of floor((a t + b) / m); a n + b fits 32 bits
 __device__ long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
     long long s = 0;
