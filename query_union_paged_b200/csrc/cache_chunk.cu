@@ -400,6 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                         if (phys < 0) ks = vl = vi = 0.f;
+                        if (!(ks < 0.f)) ks = fabsf(ks);  // -0 and what is flushed to it: not a negative scale
                     }
                     const int src = pe - have0;
                     const uint32_t live = (__ballot_sync(0xffffffffu, phys >= 0) >> src) & ((1u << PPS) - 1u);
@@ -730,19 +731,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 };
                 // a page's factor for this row, log2 of its V scale and one over it
-                const auto page = [&](int q2) {
+                const auto page = [&](int q2, bool masked) {
                     float4 v = sm.page[q2];
                     v.x *= rs;
-                    // one next to nothing (a scale or a row of zeros) stays away from 0, on the side that mask()
-                    // takes the scale to be: unseen scores are infinities, and times it have to be -inf
-                    if (fabsf(v.x) < 1e-30f) v.x = sm.page[q2].x < 0.f ? -1e-30f : 1e-30f;
+                    // one next to nothing (a scale or a row of zeros) stays away from 0 on its own side, as unseen
+                    // scores, infinities of the scale's sign, times it have to be -inf
+                    if (masked && fabsf(v.x) < 1e-30f) v.x = copysignf(1e-30f, v.x);
                     return v;
                 };
                 float bm = kNegInf;
-                const auto largest = [&](const uint32_t (&sv)[kCols], int c) {
+                const auto largest = [&](const uint32_t (&sv)[kCols], int c, bool masked) {
 #pragma unroll
                     for (int h2 = 0; h2 < kCols / TC; ++h2) {
-                        const float4 pg = page((c * kCols + h2 * TC) / T);
+                        const float4 pg = page((c * kCols + h2 * TC) / T, masked);
                         float mx[2] = {kNegInf, kNegInf};
 #pragma unroll
                         for (int t = h2 * TC; t < (h2 + 1) * TC; t += 4)
@@ -759,11 +760,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_wait_ld();
                         reg_fence<kCols>(sa);
                         tmem_ld32(s_addr + kCols * (c + 1), sb);
-                        largest(sa, c);
+                        largest(sa, c, false);
                         tmem_wait_ld();
                         reg_fence<kCols>(sb);
                         tmem_ld32(s_addr + (c + 2) % (kStep / kCols) * kCols, sa);
-                        largest(sb, c + 1);
+                        largest(sb, c + 1, false);
                     }
                     tmem_wait_ld();
                     reg_fence<kCols>(sa);
@@ -772,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int c = 0; c < kStep / kCols; ++c) {
                         tmem_ld32_wait(s_addr + kCols * c, sa);
                         mask(sa, c, true);
-                        largest(sa, c);
+                        largest(sa, c, true);
                     }
                 }
                 const bool mv = !(bm <= m + kLazy);  // or NaN, which then stays
@@ -835,16 +836,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) mbar_arrive(B.pfull(w, half));
                 };
                 if (plain) {  // the first 16 scores are there
-                    float4 pa = page(0);
+                    float4 pa = page(0, false);
 #pragma unroll 1
                     for (int t1 = 0; t1 < kStep; t1 += 32) {
                         tmem_ld16(s_addr + t1 + 16, sb);
-                        const float4 pb = T < 32 ? page((t1 + 16) / T) : pa;
+                        const float4 pb = T < 32 ? page((t1 + 16) / T, false) : pa;
                         exps(sa, t1, pa);
                         tmem_wait_ld();
                         reg_fence<16>(sb);
                         tmem_ld16(s_addr + (t1 + 32) % kStep, sa);
-                        if (T < kStep) pa = page((t1 + 32) % kStep / T);
+                        if (T < kStep) pa = page((t1 + 32) % kStep / T, false);
                         exps(sb, t1 + 16, pb);
                         tmem_wait_ld();
                         reg_fence<16>(sa);
@@ -855,8 +856,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int c = 0; c < kStep / kCols; ++c) {
                         tmem_ld32_wait(s_addr + kCols * c, sa);
                         mask(sa, c, false);
-                        exps(sa, c * kCols, page(c * kCols / T));
-                        exps(sa + 16, c * kCols + 16, page((c * kCols + 16) / T));
+                        exps(sa, c * kCols, page(c * kCols / T, true));
+                        exps(sa + 16, c * kCols + 16, page((c * kCols + 16) / T, true));
                         if (c & 1) signal(c >> 1);
                     }
                 }
