@@ -615,7 +615,8 @@ def cache_attn(cache: KVCache, Q, q_ptr, max_q: int, topk=None, softmax_scale: O
     index = cache._index
     _need(Q.dim() == 3, "Q: [Nq][Hq][128] wanted")
     Nq, Hq, _ = shape = Q.shape
-    _int32(max_q=max_q)
+    if not -1 << 31 <= max_q < 1 << 31:
+        _int32(max_q=max_q)
     _heads(Q, "Q", torch.bfloat16, (Nq, Hq, 128), index)
     _whole(q_ptr, "q_ptr", torch.int32, (cache.R + 1,), index)
     ksel = topk_p = lse_p = weight_p = None

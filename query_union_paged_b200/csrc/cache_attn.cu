@@ -79,13 +79,6 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
     return v;
 }
-// A bounded wait that the warp's lanes answer as one: a lane whose own limit had run out would leave the
-// others in shuffles, votes and products of the whole warp.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                          const CacheAttnParams& p) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.err, QUP_ERR_TIMEOUT, p.wait_limit_ns));
-}
-
 // Work units of one row tile of a request, and its row tiles.
 __device__ __forceinline__ int units_of(int len) { return (len + kUnit - 1) / kUnit; }
 __device__ __forceinline__ int tiles_of(int n, int g, int RT) { return (n * g + RT - 1) / RT; }
@@ -248,6 +241,7 @@ __global__ void __launch_bounds__(kThreads, cache_attn_ctas(NT))
 
     // ---------------------------------------------------------------- this CTA's work
     Seg sg;                  // TopK: the one segment
+    float2* mass = nullptr;  // page weights: of the segment's rows
     int list_lo = 0, list_n = 0;
     uint32_t *bits = nullptr, *masks = nullptr;
     int *before = nullptr, *pages = nullptr;
@@ -342,6 +336,9 @@ __global__ void __launch_bounds__(kThreads, cache_attn_ctas(NT))
             atomicOr(&masks[at], 1u << j);
         }
         __syncthreads();
+        if constexpr (WEIGHTS) {
+            mass = mass_of_query(p, q, h, qi - q.q0);
+        }
         sg.r = r;
         sg.q0 = qi;
         sg.n = 1;
@@ -358,6 +355,8 @@ __global__ void __launch_bounds__(kThreads, cache_attn_ctas(NT))
     if constexpr (!SPARSE) cur.begin(Start{s_start[0], s_start[1], s_start[2]});
     bool more = SPARSE;
     uint32_t it = 0;  // stages used so far: slot it % NS, parity (it / NS) & 1
+    // A wait was given up.  The lanes of a warp agree on it: one whose own limit had run out would leave the others
+    // in shuffles, votes and products of the whole warp.
     bool dead = false;
 
     if (warp == kConsumers) {
@@ -404,10 +403,9 @@ __global__ void __launch_bounds__(kThreads, cache_attn_ctas(NT))
                     if (phys < 0) msk = 0;
                 }
                 const uint32_t slot = it % NS, par = (it / NS) & 1;
-                if (!warp_wait(empty0 + 8 * slot, par ^ 1, abort_flag, p)) {
-                    dead = true;
-                    break;
-                }
+                dead = !__all_sync(0xffffffffu, mbar_wait(empty0 + 8 * slot, par ^ 1, abort_flag, p.err, QUP_ERR_TIMEOUT,
+                                                          p.wait_limit_ns));
+                if (dead) break;
                 const int src = pe - have0;
                 uint32_t bytes = 0;
                 for (int x = 0; x < nbox; ++x) {
@@ -526,29 +524,38 @@ __global__ void __launch_bounds__(kThreads, cache_attn_ctas(NT))
         const uint32_t all_rows = SPARSE ? (rows == 32 ? 0xffffffffu : (1u << rows) - 1u) : 0xffffffffu;
 
         // page weights: this tile's rows, mass_rows apart for every 16 tokens
-        size_t mass_rows = 0;
-        float2* mass = nullptr;
-        if constexpr (WEIGHTS) {
+        const int mass_rows = SPARSE ? g : sg.n * g;
+        if constexpr (WEIGHTS && !SPARSE) {
             Request q{};
-            q.q0 = SPARSE ? p.q_ptr[sg.r] : sg.q0;
-            q.n = SPARSE ? p.q_ptr[sg.r + 1] - q.q0 : sg.n;
+            q.q0 = sg.q0;
+            q.n = sg.n;
             q.p0 = sg.p0;
             q.np = sg.np;
-            mass_rows = (size_t)q.n * g;
-            mass = mass_of(p, q, sg.h, false) + (SPARSE ? (sg.q0 - q.q0) * g : row0);
+            mass = mass_of(p, q, sg.h, false) + row0;
         }
         // One turn: NG units, 16 tokens of each.  Two at a time hide each other's latencies (products in a
         // chain, conversions, the row maximum's shuffles): one warp alone keeps its scheduler a third busy.
         const auto turn = [&](auto groups) {
             constexpr int NG = decltype(groups)::value;
+            bool here = true;  // tried once, all together; waited for only where that fails
+#pragma unroll
+            for (int n = 0; n < NG; ++n) here &= mbar_try_wait(full0 + 8 * ((it + n) % NS), ((it + n) / NS) & 1);
+            if (!__all_sync(0xffffffffu, here)) {
+                here = true;
+#pragma unroll
+                for (int n = 0; n < NG; ++n)
+                    here = here && mbar_wait(full0 + 8 * ((it + n) % NS), ((it + n) / NS) & 1, abort_flag, p.err,
+                                             QUP_ERR_TIMEOUT, p.wait_limit_ns);
+                dead = !__all_sync(0xffffffffu, here);
+                if (dead) return;
+            }
             PageMeta pm[NG];
             int pos[NG];  // of the warp's first token of each
             bool live[NG], mixed[NG], any = false;
             uint32_t tile[NG];
 #pragma unroll
             for (int n = 0; n < NG; ++n) {
-                const uint32_t slot = (it + n) % NS, par = ((it + n) / NS) & 1;
-                if (!dead && !warp_wait(full0 + 8 * slot, par, abort_flag, p)) dead = true;
+                const uint32_t slot = (it + n) % NS;
                 pm[n] = meta[slot * kMaxBoxes + 16 * warp / box];
                 pos[n] = pm[n].pos + (16 * warp) % box;
                 live[n] = pm[n].mask != 0u && pos[n] < vis_any;
@@ -556,7 +563,6 @@ __global__ void __launch_bounds__(kThreads, cache_attn_ctas(NT))
                 any = any || live[n];
                 tile[n] = sbase + L::ring + slot * 2 * kTile;
             }
-            if (dead) return;
             if (any) {
                 // ---- S^T = K Q^T: tokens i and i + 8 of the warp, d = 32 q4 .. + 31 of each in two loads
                 float c[NG][NT][4];
@@ -1002,18 +1008,26 @@ __global__ void __launch_bounds__(32 * kWeightWarps) cache_weight_kernel(const _
             const int rows = q.n * g;
             const bool big = !SPARSE && rows >= p.big_rows;
             const int total = rows * (big ? 1 : T / 16);
-            const float2* src = mass_of(p, q, h, big) + (size_t)pg * total;
+            const float2* src = SPARSE ? nullptr : mass_of(p, q, h, big) + (size_t)pg * total;
             const uint32_t* bits = SPARSE ? p.ws_bits + (size_t)(q.p0 / 32 + r) * p.max_q * p.c.Hkv : nullptr;
             for (int e = pg * T < q.len ? sub : total; e < total; e += S) {
                 const int grp = e / rows, row = e - grp * rows, qi = row / g, j = row - qi * g;
+                float2 a = make_float2(0.f, 0.f);
+                float l2 = 0.f;
+                const auto lse = [&] { return p.ws_lse[(size_t)(q.q0 + qi) * p.Hq + h * g + j]; };
+                if (!SPARSE) {  // loaded whether the row sees the page or not, so that the loads wait for no test
+                    a = src[e];
+                    l2 = lse();
+                }
                 const int pos = pg * T + 16 * grp;
                 // the attention kernel reads whole tiles: what a row does not see it has as zero, but
                 // 16 tokens that no row of its tile sees it leaves out
                 if (pos >= q.len - q.n + qi + 1) continue;
-                if (SPARSE && !((bits[((size_t)qi * p.c.Hkv + h) * ((q.np + 31) / 32) + (pg >> 5)] >> (pg & 31)) & 1u))
-                    continue;
-                const float2 a = src[e];
-                const float l2 = p.ws_lse[(size_t)(q.q0 + qi) * p.Hq + h * g + j];
+                if (SPARSE) {
+                    if (!((bits[((size_t)qi * p.c.Hkv + h) * ((q.np + 31) / 32) + (pg >> 5)] >> (pg & 31)) & 1u)) continue;
+                    a = mass_of_query(p, q, h, qi)[((size_t)pg * (T / 16) + grp) * g + j];
+                    l2 = lse();
+                }
                 // a row whose running maximum was still -inf has 0 here; NaN stays NaN
                 sum += a.x == 0.f ? 0.f : a.x * ex2((a.y == kNegInf ? 0.f : a.y - kOffset) - l2);
             }

@@ -92,14 +92,20 @@ __device__ __forceinline__ unsigned request_fault(const CacheAttnParams& p, cons
     if (!q.ok || q.n > p.max_q) return QUP_ERR_GROUP;
     return q.np > p.max_pages ? QUP_ERR_CAPACITY : 0u;
 }
-// Page weights: the sums of request q's rows of KV head h, [page][T / 16, or 1 if big][n * g].  Requests lie
-// one behind the other either by their pages, with room for the longest one's rows, or by their rows, with room for
-// the most pages: what takes less for the whole batch.
+// Page weights: where a request's sums lie.  Requests follow each other either by their pages, with room for the longest
+// one's rows (per != 0), or by their rows, with room for the most pages: what takes less for the whole batch.
+// All pages: the sums of request q's rows of KV head h, [page][T / 16, or 1 if big][n * g].
 __device__ __forceinline__ float2* mass_of(const CacheAttnParams& p, const Request& q, int h, bool big) {
     const int per = big ? p.mass_chunk_per : p.mass_per;
     const size_t at = per ? ((size_t)q.p0 * p.c.Hkv + (size_t)h * q.np) * per
                           : ((size_t)q.q0 * p.c.Hkv + (size_t)h * q.n) * p.g * p.max_pages;
     return big ? p.mass_chunk + at : p.mass + at * (p.c.T / 16);
+}
+// TopK pages: those of the request's query i, [page][T / 16][g].
+__device__ __forceinline__ float2* mass_of_query(const CacheAttnParams& p, const Request& q, int h, int i) {
+    const size_t at = p.mass_per ? (size_t)q.p0 * p.c.Hkv * p.max_q + ((size_t)h * p.max_q + i) * q.np
+                                 : ((size_t)(q.q0 + i) * p.c.Hkv + h) * p.max_pages;
+    return p.mass + at * (p.c.T / 16) * p.g;
 }
 // Rows of faulty requests (`big`: those that would be the chunk kernel's) get O = 0 and lse = -inf: the CTAs
 // take the requests in turn.
