@@ -455,8 +455,9 @@ int qup_cache_append(const qup_cache* cache, const void* k_new, const void* v_ne
  *              the request's queries and the KV head's Q heads give each page
  *              of the table, added up (0 for pages without visible tokens)
  *   ws         device scratch of the size qup_cache_attn_workspace reports for
- *              the same cache sizes, Nq, max_q, Hq and page_weight (0: none; 1:
- *              with page weights; 2: likewise, for calls without topk only):
+ *              the same cache sizes, Nq, max_q, Hq and page_weight (0: none; 2:
+ *              with page weights, for calls without topk only; else with page
+ *              weights, for any call):
  *              5 MB, or 44 where a request may have more than 16 rows (query and
  *              Q head) of a KV head.  Page weights add 8 bytes for each row and
  *              page of such requests, min(max_q * total_pages, Nq * max_pages)

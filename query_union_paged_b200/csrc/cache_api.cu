@@ -161,7 +161,6 @@ int qup_cache_append(const qup_cache* cache, const void* k_new, const void* v_ne
 int qup_cache_attn_workspace(const qup_cache* cache, int Nq, int max_q, int Hq, int page_weight, size_t* ws_bytes) {
     const int rc = check_attn_sizes(cache, Nq, max_q, Hq);
     if (rc) return rc;
-    if (page_weight < 0 || page_weight > 2) return QUP_ERR_ARG;
     if (ws_bytes) {
         *ws_bytes = attn_ws_layout(cache, Nq, max_q, Hq, page_weight != 0, false).total;
         if (page_weight != 2)  // TopK calls too

@@ -28,7 +28,7 @@
 // (query, KV head), its distinct pages cut into an equal share per CTA.
 //
 // Bound by DRAM: 2 * 128 bytes per token and KV head.  16 requests of 33K to 64K tokens, 8 KV heads, 32
-// heads: 265 to 280 us, 5.7 to 6.0 TB/s (0.86 to 0.91 of a copy); a TopK call of 32 pages of 64 tokens 35 us,
+// heads: 258 to 280 us, 5.7 to 6.1 TB/s (0.86 to 0.94 of a copy); a TopK call of 32 pages of 64 tokens 35 us,
 // 3.8 TB/s (finding a query's pages costs a CTA about 5 us before its first load).
 #include <algorithm>
 #include <cstdint>

@@ -28,7 +28,7 @@
 // Bound: a step of 256 rows takes about 4,600 cycles.  The two warpgroups' softmax takes 2,500 to 3,200 of
 // them together (their exponentials alone 1,800 to 2,100, of which the MUFU unit 1,790), the tensor
 // cores 2,050; what does not overlap is the way from P to the next S (O update, S, two completions of
-// 200 to 400 cycles each).  1,024 queries x 32 heads behind 16K tokens: 335 to 340 us, 0.84 PFLOP/s.
+// 200 to 400 cycles each).  1,024 queries x 32 heads behind 16K tokens: 316 to 328 us, 0.88 PFLOP/s.
 // Measured and left out: loops unrolled over a step (instruction fetch: +23 %), the warpgroups taking
 // turns (+57 %: one alone is hardly faster than both together), half steps with S, P and O update of their
 // own (+14 %: products of 64 columns take as long to issue as of 128), a step's tokens split over both
