@@ -435,8 +435,8 @@ int qup_cache_append(const qup_cache* cache, const void* k_new, const void* v_ne
  * token may be off by 2^-33 * 448 * the largest V scale of the pages that the
  * row sees: one page whose scale an outlier made larger than the others' by
  * 2^22 or more costs those bits, also where the outlier itself is not seen.  A
- * token's part in the sum of weights, lse and page_weight is lost below 2^-134 *
- * that scale / its own page's.  For requests of more than 16 rows of a KV head Q
+ * token's part in the sum of weights is lost below 2^-119 * that scale / its
+ * own page's, in page_weight below 2^-134 of it.  For requests of more than 16 rows of a KV head Q
  * is held exactly down to 2^-9 of the row's largest element and within 2^-17
  * of it below.  Sums are fp32.
  *   Q          device bf16 [Nq][Hq][128], q_stride elements from one query to

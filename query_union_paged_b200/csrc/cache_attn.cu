@@ -1029,7 +1029,10 @@ __global__ void __launch_bounds__(32 * kWeightWarps) cache_weight_kernel(const _
                     l2 = lse();
                 }
                 // a row whose running maximum was still -inf has 0 here; NaN stays NaN
-                sum += a.x == 0.f ? 0.f : a.x * ex2((a.y == kNegInf ? 0.f : a.y - kOffset) - l2);
+                // the factor in two halves: a.x is large where the page's V scale is small, and the whole factor
+                // would be lost below 2^-126 where their product is not
+                const float half = ex2(0.5f * ((a.y == kNegInf ? 0.f : a.y - kOffset) - l2));
+                sum += a.x == 0.f ? 0.f : a.x * half * half;
             }
         }
         for (int s = S / 2; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);

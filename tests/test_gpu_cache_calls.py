@@ -314,3 +314,18 @@ def test_page_weights_stay_in_their_workspace(T, lens, ns, topk):
     with pytest.raises(qup.QupError):
         qup.cache_attn(cache, qt, ptr, max(ns), topk=None if tk is None else torch.from_numpy(tk).cuda(),
                        page_weight=again, workspace=small[:4 << 20])  # less than the smallest of all
+
+
+@pytest.mark.parametrize("n", [1, 20])
+def test_small_weights_of_pages_of_zero_scale(n):
+    """A page of zeros (V scale 0) whose softmax weight is next to nothing, before and behind the pages that carry the
+    row: its weight is there down to what its exponentials can hold."""
+    c = Case(130, [300, 290], T=32)
+    for r in range(2):
+        p = c.table[c.page_ptr[r]:]
+        for x in (0, 4):
+            c.vs[p[x]], c.V[p[x]], c.ks[p[x]] = 0.0, 0, 0.0  # scores of 0: a weight of 32 e^-lse
+    o, lse, w, ref = _run_attn(c, [n, n], 4, qstd=14.0 if n == 1 else 17.0)
+    small = ref["weight"][c.page_ptr[:2]]
+    assert 2.0 ** -66 < small.min() < 2.0 ** -57 and small.max() < 2.0 ** -45
+    _check_attn(o, lse, w, ref, 300, n)
