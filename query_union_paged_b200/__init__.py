@@ -469,10 +469,13 @@ def _need(ok, what: str):
         raise ValueError(what)
 
 
+_2_31 = 1 << 31
+
+
 def _int32(**numbers):
     """The numbers fit the C call's int (ctypes would cut them without a word)."""
     for name, x in numbers.items():
-        _need(-1 << 31 <= x < 1 << 31, f"{name} {x}: out of 32 bits")
+        _need(-_2_31 <= x < _2_31, f"{name} {x}: out of 32 bits")
 
 
 def _whole(t, name: str, dtype, shape, index: int):
@@ -615,7 +618,7 @@ def cache_attn(cache: KVCache, Q, q_ptr, max_q: int, topk=None, softmax_scale: O
     index = cache._index
     _need(Q.dim() == 3, "Q: [Nq][Hq][128] wanted")
     Nq, Hq, _ = shape = Q.shape
-    if not -1 << 31 <= max_q < 1 << 31:
+    if not -_2_31 <= max_q < _2_31:
         _int32(max_q=max_q)
     _heads(Q, "Q", torch.bfloat16, (Nq, Hq, 128), index)
     _whole(q_ptr, "q_ptr", torch.int32, (cache.R + 1,), index)
@@ -660,7 +663,8 @@ def cache_evict(cache: KVCache, page_weight, acc, budget: int, sink: int = 1, re
     """
     import torch
     index, n = cache._index, cache.total_pages
-    _int32(budget=budget, sink=sink, recent=recent)
+    if not (-_2_31 <= budget < _2_31 and -_2_31 <= sink < _2_31 and -_2_31 <= recent < _2_31):
+        _int32(budget=budget, sink=sink, recent=recent)
     _whole(page_weight, "page_weight", torch.float32, (n, cache.Hkv), index)
     _whole(acc, "acc", torch.float32, (n,), index)
     if out is None:
